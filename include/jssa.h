@@ -89,7 +89,8 @@ enum {
   JSSA_DEV_BAD_SEQ_LEN = 1, /* a seq_lens[b] outside [0, T_cap] (clamped)        */
   JSSA_DEV_BAD_INDEX = 2,   /* an index outside its candidate range (skipped)    */
   JSSA_DEV_BAD_NSEL = 4,    /* an n_sel outside [0, k] (clamped)                 */
-  JSSA_DEV_TIMEOUT = 8      /* a bounded wait gave up                            */
+  JSSA_DEV_TIMEOUT = 8,     /* a bounded wait gave up                            */
+  JSSA_DEV_NO_PAGES = 16    /* too few free pages or table entries (no change)   */
 };
 
 /*
@@ -317,6 +318,144 @@ JSSA_API jssa_status jssa_dense_decode(const jssa_layout* L, const void* Q, cons
 JSSA_API jssa_status jssa_calibrate_workspace_size(const jssa_layout* L, size_t* bytes);
 JSSA_API jssa_status jssa_calibrate(const jssa_layout* L, const void* Qc, const void* K, int64_t n_tokens,
                                     float* P, double* eigvals, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * ---- Paged caches ------------------------------------------------------------------
+ * K and V rows in pools of fixed-size pages; a page table names each sequence's pages in
+ * order.  The pages of one table serve every layer: the bookkeeping calls run once per step,
+ * append, attention and page copies once per layer's pools.
+ *   K, V        element (page p, head h, row s, i) at K[p*k_stride[0] + h*k_stride[1] + s*k_stride[2] + i]
+ *               (bf16, i < d; V likewise): heads outside or inside the rows of a page
+ *   page_table  device int32 [B, max_pages], contiguous: token t of sequence b is row
+ *               t % page_size of page page_table[b, t / page_size]; -1 marks an entry without a page
+ *   ref_count   device int32 [n_pages]: table entries that name the page (0: free)
+ *   seq_lens    device int32 [B]: tokens in the cache, at most max_pages * page_size
+ * Q heads as elsewhere: query head hq belongs to KV head hq / G, G = Hq / Hkv.
+ * Supported: d in {64, 128, 256}, 1 <= G <= 128, page_size a multiple of 16, B <= 1024,
+ * n_pages < 2^31 and max_pages * page_size < 2^31.  Pool pointers 16-byte aligned, strides
+ * multiples of 8 elements; pages, heads and rows of a pool must not overlap.
+ * A contiguous cache [B, Hkv, T_cap, d] (T_cap a multiple of 16) is a pool of B pages of T_cap
+ * rows with the table page_table[b, 0] = b: the calls below then fill and read the caches of
+ * the calls above.
+ *
+ * "Newest tokens": the calls that bring or read new tokens take them packed, sequence after
+ * sequence: token row i of sequence b is row q_begin[b] + i for i < q_begin[b+1] - q_begin[b]
+ * (q_begin: device int32 [B+1], ascending, q_begin[B] <= n_tokens) and stands at position
+ * seq_lens[b] - (q_begin[b+1] - q_begin[b]) + i: seq_lens counts the new tokens.  A sequence
+ * may have none.  Rows at and past q_begin[B] are neither read nor written.
+ *
+ * Workspace: jssa_paged_workspace_size() bytes, zeroed once with jssa_workspace_init(); it holds
+ * the status word and scratch, and every call leaves it ready for the next.  Calls that may
+ * overlap on the GPU (other streams) need a workspace each.
+ *
+ * Checks on the device: a sequence whose length is outside [0, max_pages * page_size], or whose
+ * rows in q_begin are out of order, past n_tokens or more than its length, raises
+ * JSSA_DEV_BAD_SEQ_LEN and is left out (append and attention write none of its rows; the page
+ * calls clamp the length).  A page-table entry that a call needs and that is no page raises
+ * JSSA_DEV_BAD_INDEX (its tokens are not written; attention leaves them out).
+ */
+typedef struct {
+  int32_t B;          /* sequences: rows of the page table                 */
+  int32_t Hq, Hkv, d; /* heads and head dim                                */
+  int32_t page_size;  /* tokens per page                                   */
+  int32_t n_pages;    /* pages in each pool                                */
+  int32_t max_pages;  /* page-table entries per sequence                   */
+  int32_t out_dtype;  /* JSSA_OUT_F32 or JSSA_OUT_BF16 (attention)         */
+  int64_t k_stride[3]; /* page, head, row                                  */
+  int64_t v_stride[3];
+} jssa_paged_layout;
+
+/*
+ * Bytes of workspace for the calls below, with at most max_q_len new tokens per sequence in
+ * jssa_paged_attn (0: none of its calls use this workspace), on the current device.
+ */
+JSSA_API jssa_status jssa_paged_workspace_size(const jssa_paged_layout* L, int32_t max_q_len, size_t* bytes);
+
+/*
+ * Append: writes the newest tokens' key and value rows into their pages.
+ *   K_new, V_new  device bf16, element (row i, head h, e) at K_new[i*new_stride + h*d + e]
+ *                 (new_stride >= Hkv * d, a multiple of 8: rows may be slices of a fused projection)
+ * A page that two sequences share must be split before it is written (jssa_pages_reserve).
+ */
+JSSA_API jssa_status jssa_paged_append_kv(const jssa_paged_layout* L, const void* K_new, const void* V_new,
+                                          int64_t new_stride, int64_t n_tokens, void* K, void* V,
+                                          const int32_t* page_table, const int32_t* q_begin, const int32_t* seq_lens,
+                                          void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Attention of the newest tokens (one per sequence, a few, or a chunk of a prompt) over the
+ * paged cache, their own rows included.  The query at position p attends
+ *   t <= p                                   (window = 0)
+ *   t <= p  and  (t > p - window or t < n_sinks)   (window > 0: the sliding window and the sinks)
+ * logits = sm_scale * q . k_t, softmax and sums in fp32; O = sum_t p_t v_t / sum_t p_t.
+ *   Q    device bf16, element (row i, head hq, e) at Q[i*q_stride + hq*d + e], q_stride >= Hq*d, a
+ *        multiple of 8; 16-byte aligned
+ *   O    [n_tokens, Hq, d] fp32 or bf16 (out_dtype), contiguous, 16-byte aligned
+ *   lse  [n_tokens, Hq] fp32 natural-log log-sum-exp (optional)
+ * A query that sees nothing gets O = 0 and lse = -inf.  max_q_len bounds every sequence's new
+ * tokens (a sequence with more is left out and raises JSSA_DEV_BAD_SEQ_LEN).  Pages that no
+ * query of the call sees need not exist; cache rows that no query of the call sees may hold
+ * anything, rows that one sees must be finite.
+ */
+JSSA_API jssa_status jssa_paged_attn(const jssa_paged_layout* L, const void* Q, int64_t q_stride, int64_t n_tokens,
+                                     int32_t max_q_len, const void* K, const void* V, const int32_t* page_table,
+                                     const int32_t* q_begin, const int32_t* seq_lens, int32_t window, int32_t n_sinks,
+                                     float sm_scale, void* O, float* lse, void* workspace, size_t ws_bytes,
+                                     void* stream);
+
+/*
+ * Fork: sequence dst[i] becomes a copy of sequence src[i] that shares its pages (each counted
+ * once more); n entries, device int32.  An entry with src[i] < 0 is skipped.  An entry is
+ * skipped and raises JSSA_DEV_BAD_INDEX if src[i] or dst[i] is no sequence, dst[i] is not
+ * empty (seq_lens 0), an earlier entry names the same dst, or the call forks from dst[i] or to
+ * src[i].
+ */
+JSSA_API jssa_status jssa_pages_fork(const jssa_paged_layout* L, const int32_t* src, const int32_t* dst, int32_t n,
+                                     int32_t* page_table, int32_t* ref_count, int32_t* seq_lens, void* workspace,
+                                     size_t ws_bytes, void* stream);
+
+/*
+ * Reserve: makes room for n_new[b] (device int32 [B]) more tokens of every sequence and adds them to
+ * seq_lens.  In sequence order, a partly filled last page that others share is exchanged for a
+ * page of the sequence's own (copy on write: copy_src[b], copy_dst[b] name the pages to copy
+ * with jssa_pages_copy before the append, -1 where there is none; device int32 [B]), then
+ * pages are taken for the new tokens; the lowest free pages first.  When free pages or table
+ * entries do not suffice, or a partly filled last page is missing from the table, nothing
+ * changes, every copy entry is -1 and JSSA_DEV_NO_PAGES is raised.  A negative n_new or a bad
+ * sequence length raises JSSA_DEV_BAD_SEQ_LEN and counts as no new tokens.
+ */
+JSSA_API jssa_status jssa_pages_reserve(const jssa_paged_layout* L, const int32_t* n_new, int32_t* page_table,
+                                        int32_t* ref_count, int32_t* seq_lens, int32_t* copy_src, int32_t* copy_dst,
+                                        void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Release: sequences with ended[b] != 0 (device int32 [B], nullable: none) give up all their pages and
+ * become empty.  With window > 0 the other sequences give up the pages that lie wholly behind
+ * the last `window` tokens and hold none of the first n_sinks.  Entries become -1; a page
+ * is free when no entry names it.
+ */
+JSSA_API jssa_status jssa_pages_release(const jssa_paged_layout* L, const int32_t* ended, int32_t window,
+                                        int32_t n_sinks, int32_t* page_table, int32_t* ref_count, int32_t* seq_lens,
+                                        void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Compact: with m pages in use, those at or above m are given the free pages below m, both in
+ * ascending order, at most max_moves of them.  Rewrites page_table and ref_count; src and dst
+ * (device int32 [max_moves]) name the pages to copy with jssa_pages_copy before the cache is
+ * used again, -1 past n_moves[0] (device int32 [1]).
+ */
+JSSA_API jssa_status jssa_pages_compact(const jssa_paged_layout* L, int32_t* page_table, int32_t* ref_count,
+                                        int32_t* src, int32_t* dst, int32_t max_moves, int32_t* n_moves,
+                                        void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Copy pages of both pools: page dst[i] = page src[i] for i < n, or for i < min(n, count[0]) with
+ * count (device int32, nullable).  Negative entries are skipped, entries past the pool are
+ * skipped and raise JSSA_DEV_BAD_INDEX.  No page may be named twice as dst, or as both.
+ */
+JSSA_API jssa_status jssa_pages_copy(const jssa_paged_layout* L, void* K, void* V, const int32_t* src,
+                                     const int32_t* dst, int32_t n, const int32_t* count, void* workspace,
+                                     size_t ws_bytes, void* stream);
 
 /*
  * Zero a freshly allocated workspace (asynchronously on `stream`): required once before

@@ -22,14 +22,15 @@ KP_BF16, KP_FP8_E4M3 = 0, 1
 STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported shape or mode", 3: "workspace missing, misaligned or too small",
           4: "CUDA error", 5: "device-side check failed", 6: "bounded wait timed out",
           7: "beyond the built-in scratch of the allocation-free entry point"}
-DEV_BAD_SEQ_LEN, DEV_BAD_INDEX, DEV_BAD_NSEL, DEV_TIMEOUT = 1, 2, 4, 8
+DEV_BAD_SEQ_LEN, DEV_BAD_INDEX, DEV_BAD_NSEL, DEV_TIMEOUT, DEV_NO_PAGES = 1, 2, 4, 8, 16
 
 EXPORTS = ("jssa_status_string", "jssa_version", "jssa_workspace_size", "jssa_project_keys", "jssa_score",
            "jssa_topk", "jssa_topk_noalloc", "jssa_select", "jssa_indexed_attn", "jssa_decode_step",
            "jssa_dense_decode", "jssa_gather_size", "jssa_gather_decode", "jssa_calibrate_workspace_size",
            "jssa_calibrate", "jssa_vote_select",
            "jssa_workspace_init", "jssa_read_device_status", "jssa_test_withhold_copy", "jssa_append_kv",
-           "jssa_copy_mapped")
+           "jssa_copy_mapped", "jssa_paged_workspace_size", "jssa_paged_append_kv", "jssa_paged_attn",
+           "jssa_pages_fork", "jssa_pages_reserve", "jssa_pages_release", "jssa_pages_compact", "jssa_pages_copy")
 
 
 class JssaError(RuntimeError):
@@ -46,6 +47,7 @@ class Layout(C.Structure):
 
 
 _lib = None
+SIGNATURE_SOURCES = []   # functions that give further entry points' signatures (_paged.py)
 
 
 def load(path: str = LIB_PATH):
@@ -82,6 +84,8 @@ def load(path: str = LIB_PATH):
         "jssa_append_kv": (C.c_int, [LP, vp, vp, vp, vp, vp, vp]),
         "jssa_copy_mapped": (C.c_int, [vp, vp, C.c_size_t, vp]),
     }
+    for more in SIGNATURE_SOURCES:
+        sig.update(more())
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
         fn.restype = res

@@ -5,32 +5,15 @@
 #include <cstring>
 
 #include "jssa.h"
+#include "api_util.h"
 #include "common.cuh"
 #include "launch.h"
 
 namespace jssa {
 namespace {
 
-constexpr size_t kAlign = 256;
-constexpr int kMaxDevices = 64;
 constexpr int64_t kMaxK = 1 << 24;
 constexpr int kMaxPrologueRows = 16;  // appended rows projected inside the step prologue
-
-size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
-
-int num_sms_current() {
-  static int cache[kMaxDevices] = {0};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return -1;
-  if (cache[dev] == 0) {
-    int n = 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return -1;
-    cache[dev] = n;
-  }
-  return cache[dev];
-}
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 bool is_pow2_in(int x, int lo, int hi) { return x >= lo && x <= hi && (x & (x - 1)) == 0; }
 
@@ -142,12 +125,6 @@ jssa_status get_ws(const jssa_layout* L, int64_t k, int64_t window, void* ws, si
 __global__ void arm_wait_test_kernel(int* status, int limit_us) {
   status[2] = limit_us;
   status[1] = 1;
-}
-
-jssa_status cu(cudaError_t e) {
-  if (e == cudaSuccess) return JSSA_OK;
-  if (e == cudaErrorNotSupported) return JSSA_ERR_UNSUPPORTED;
-  return JSSA_ERR_CUDA;
 }
 
 ProjectArgs project_args(const jssa_layout* L, const void* K, const float* P, void* Kp, const int32_t* t_begin,
@@ -380,7 +357,7 @@ const char* jssa_status_string(jssa_status s) {
   return "unknown status";
 }
 
-int32_t jssa_version(void) { return 10200; }
+int32_t jssa_version(void) { return 10300; }
 
 jssa_status jssa_workspace_size(const jssa_layout* L, int32_t k, int32_t window, size_t* bytes) {
   jssa_status st = check_layout(L);

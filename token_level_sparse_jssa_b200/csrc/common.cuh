@@ -21,6 +21,7 @@ enum : int {
   DEVFLAG_BAD_INDEX = 2,     // an index outside the candidate range (skipped)
   DEVFLAG_BAD_NSEL = 4,      // n_sel outside [0, k] (clamped)
   DEVFLAG_TIMEOUT = 8,       // a bounded wait gave up
+  DEVFLAG_NO_PAGES = 16,     // too few free pages or table entries (nothing changed)
 };
 
 __device__ __forceinline__ void flag_error(int* status, int bit) {

@@ -218,4 +218,60 @@ cudaError_t launch_attention(const AttnArgs& a, cudaStream_t s);   // GQA path
 int mla_split_groups(int B, int num_sms);
 cudaError_t launch_mla_split(const AttnArgs& a, bool dense, cudaStream_t s);
 
+// ---- Paged caches (pages.cu, paged_attn.cu)
+struct PagePool {
+  void* K;
+  int64_t ks[3];  // page, head, row (elements)
+  void* V;
+  int64_t vs[3];
+  int Hkv, d, page_size, n_pages;
+};
+struct PageBook {
+  int32_t* table;      // [B, max_pages]
+  int32_t* ref;        // [n_pages]
+  int32_t* seq_lens;   // [B]
+  int B, max_pages, page_size, n_pages;
+  int* status;
+};
+struct PagedAppendArgs {
+  PagePool pool;
+  const void* K_new;
+  const void* V_new;
+  int64_t new_stride, n_tokens;
+  const int32_t* table;
+  const int32_t* q_begin;
+  const int32_t* seq_lens;
+  int B, max_pages;
+  int* status;
+};
+cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t s);
+cudaError_t launch_pages_fork(const PageBook& k, const int32_t* src, const int32_t* dst, int n, cudaStream_t s);
+// growers: [n_pages, 2] zero on entry and exit; free_list: [n_pages]
+cudaError_t launch_pages_reserve(const PageBook& k, const int32_t* n_new, int32_t* copy_src, int32_t* copy_dst,
+                                 int32_t* growers, int32_t* free_list, cudaStream_t s);
+cudaError_t launch_pages_release(const PageBook& k, const int32_t* ended, int window, int n_sinks, cudaStream_t s);
+// map: [n_pages]
+cudaError_t launch_pages_compact(const PageBook& k, int32_t* src, int32_t* dst, int max_moves, int32_t* n_moves,
+                                 int32_t* map, cudaStream_t s);
+cudaError_t launch_pages_copy(const PagePool& p, const int32_t* src, const int32_t* dst, int n, const int32_t* count,
+                              int* status, int num_sms, cudaStream_t s);
+
+struct PagedAttnArgs {
+  PagePool pool;
+  const void* Q;
+  int64_t q_stride, n_tokens;
+  int max_q_len;
+  const int32_t* table;
+  const int32_t* q_begin;
+  const int32_t* seq_lens;
+  int B, Hq, max_pages;
+  int window, n_sinks;
+  float sm_scale;
+  void* O;
+  float* lse;
+  int out_bf16;
+  int* status;
+};
+cudaError_t launch_paged_attn(const PagedAttnArgs& a, int num_sms, cudaStream_t s);
+
 }  // namespace jssa
