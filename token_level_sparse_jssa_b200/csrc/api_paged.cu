@@ -27,7 +27,7 @@ jssa_status check_paged(const jssa_paged_layout* L) {
   if (L->B > 1024 || L->Hq > 65535 || L->Hq / L->Hkv > 128) return JSSA_ERR_UNSUPPORTED;
   if (L->d != 64 && L->d != 128 && L->d != 256) return JSSA_ERR_UNSUPPORTED;
   if (L->page_size % 16) return JSSA_ERR_UNSUPPORTED;
-  if (static_cast<int64_t>(L->max_pages) * L->page_size > kInt31 ||
+  if (static_cast<int64_t>(L->max_pages) * L->page_size > (int64_t(1) << 30) ||
       static_cast<int64_t>(L->B) * L->max_pages > kInt31 ||
       static_cast<int64_t>(L->Hkv) * L->page_size * (L->d / 8) > kInt31 - 4096)
     return JSSA_ERR_UNSUPPORTED;
@@ -39,13 +39,16 @@ struct PagedWorkspace {
   int32_t* growers;    // [n_pages, 2], zero between calls
   int32_t* free_list;  // [n_pages]
   int32_t* map;        // [n_pages + 1]
+  int32_t* counters;   // [num_sms], zero between calls
+  float2* part_ml;     // [2 num_sms][rows_cap]
+  float* part_o;       // [2 num_sms][rows_cap][d]
+  int rows_cap;
   size_t bytes;
 };
 
 jssa_status carve_paged(const jssa_paged_layout* L, int max_q_len, void* base, PagedWorkspace* w) {
   const int num_sms = num_sms_current();
   if (num_sms <= 0) return JSSA_ERR_CUDA;
-  (void)max_q_len;
   size_t off = 0;
   char* p = static_cast<char*>(base);
   auto take = [&](size_t n) {
@@ -58,6 +61,11 @@ jssa_status carve_paged(const jssa_paged_layout* L, int max_q_len, void* base, P
   w->growers = reinterpret_cast<int32_t*>(take(2 * n * sizeof(int32_t)));
   w->free_list = reinterpret_cast<int32_t*>(take(n * sizeof(int32_t)));
   w->map = reinterpret_cast<int32_t*>(take((n + 1) * sizeof(int32_t)));
+  w->counters = reinterpret_cast<int32_t*>(take(num_sms * sizeof(int32_t)));
+  w->rows_cap = paged_attn_rows(L->d, L->Hq / L->Hkv, max_q_len);
+  const size_t rows = static_cast<size_t>(2 * num_sms) * w->rows_cap;
+  w->part_ml = reinterpret_cast<float2*>(take(rows * sizeof(float2)));
+  w->part_o = reinterpret_cast<float*>(take(rows * L->d * sizeof(float)));
   w->bytes = off;
   return JSSA_OK;
 }
@@ -189,6 +197,10 @@ jssa_status jssa_paged_attn(const jssa_paged_layout* L, const void* Q, int64_t q
   a.lse = lse;
   a.out_bf16 = (L->out_dtype == JSSA_OUT_BF16);
   a.status = w.status;
+  a.part_o = w.part_o;
+  a.part_ml = w.part_ml;
+  a.counters = w.counters;
+  a.rows_cap = w.rows_cap;
   return cu(launch_paged_attn(a, num_sms_current(), static_cast<cudaStream_t>(stream)));
 }
 

@@ -271,7 +271,14 @@ struct PagedAttnArgs {
   float* lse;
   int out_bf16;
   int* status;
+  // partial outputs of cut items, two per CTA: [2 num_sms][rows_cap] rows; [num_sms] zero on entry and exit
+  float* part_o;
+  float2* part_ml;
+  int32_t* counters;
+  int rows_cap;
 };
+int paged_attn_tile_tokens(int G);
+int paged_attn_rows(int d, int G, int64_t max_q_len);  // rows of an item, at most
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, int num_sms, cudaStream_t s);
 
 }  // namespace jssa

@@ -1,93 +1,851 @@
 // Attention of each sequence's newest tokens over a paged cache: causal, with an optional
-// sliding window and sinks.
+// sliding window and sinks, on the fifth-generation tensor cores.
 //
-// One block per (token row, query head); each of its 4 warps takes every fourth visible
-// position, with a lane's share of the head dims in registers and an online softmax in fp32;
-// the warps' states are merged in shared memory.
+//   o = sum_t p_t v_t / sum_t p_t,  p_t = exp(sm_scale q . k_t - m),  t over the visible tokens
+//
+// in one pass over K and V with a running maximum m and sum per row.  The query rows of one KV
+// head's group stand side by side: row r of a query tile is token r / G, head r % G of the group,
+// so that one tile of 128 rows serves a single token of 128 heads and 128 tokens of one head
+// alike, and a K/V row is read once for the whole group.
+//
+// Items: (sequence, KV head, block of query tiles).  An item's keys are a list of 128 (64 for
+// d = 256) at a time, its tiles: the sink pages' first rows, then the rows from the first
+// query's window to the last query.  All tiles of all items form one line that is cut into equal
+// pieces, one per CTA (one CTA per SM): long caches with few rows are split, ragged batches are
+// balanced, and the host needs no lengths.  An item that is cut leaves unnormalised partial
+// outputs with their maxima and sums in the workspace; the CTA that finishes it last merges
+// them, in the order of the cuts, so results do not depend on timing.
+//
+// Per tile:  S = Q K^T (M = 128 rows, N = keys), P = exp2(S - m) by one thread per row, written
+// over S in tensor memory, O += P V with P as the tensor-memory operand.  Two softmax
+// warpgroups (one for d = 256) take turns with the tensor core: items of more than one query tile
+// give each warpgroup a tile of rows; items of one give them every other tile of keys, and the
+// two halves are added at the end.  O stays in tensor memory; the maximum that P refers to
+// moves only when a row's grows by more than 2^8, so O is rarely rescaled.
+//
+// P is rounded to bf16 for the product with V, which adds about as much error as rounding the
+// output to bf16; with an fp32 output the remainder p - bf16(p) takes a second product, so that
+// the output is good to about 2^-16.  Maxima, sums and O are fp32.
+//
+// Warps: softmax, then one that issues the MMAs, one that loads (TMA boxes of at most 128 rows
+// that never cross a page), and one that zeroes the V rows of a loaded tile that no query of
+// the item sees: P is 0 there, but such rows may hold infinities or NaN.
+// Every wait is bounded; on a timeout the kernel raises DEVFLAG_TIMEOUT, all roles leave their
+// loops, copies and MMAs in flight are drained, and tensor memory is freed.
+#include <cuda.h>
+
 #include "common.cuh"
 #include "launch.h"
 #include "paged.cuh"
+#include "tcgen05.cuh"
 
 namespace jssa {
 namespace {
 
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kPaOCol = 256;   // first TMEM column of O; S (and P over it) below
+constexpr float kPaRescale = 8.f;   // log2 margin before the running maximum moves
+constexpr int kPaBadRing = 16;      // tiles whose missing pages are remembered
+constexpr float kLog2e = 1.4426950408889634f;
+
 template <int D>
-__global__ void __launch_bounds__(128) paged_attn_simple_kernel(PagedAttnArgs a) {
-  constexpr int PL = D / 32;
-  __shared__ float m_s[4], l_s[4], o_s[4][D];
-  const int64_t i = blockIdx.x;
-  const int hq = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int b = sequence_of(a.q_begin, a.B, i);
-  const NewTokens r = new_tokens(a.q_begin, a.seq_lens, b, static_cast<int64_t>(a.max_pages) * a.pool.page_size,
-                                 a.n_tokens, a.max_q_len, a.status);
-  if (i < r.q0 || i >= r.q0 + r.nq) return;
-  const int64_t pos = r.len - r.nq + (i - r.q0);
-  const int64_t win = a.window > 0 ? max64(0, pos + 1 - a.window) : 0;
-  const int64_t sinks = min64(win, a.n_sinks);  // visible: [0, sinks) and [win, pos]
-  const int64_t n = sinks + pos + 1 - win;
-  const int h = hq / (a.Hq / a.pool.Hkv);
-  const __nv_bfloat16* K = static_cast<const __nv_bfloat16*>(a.pool.K) + h * a.pool.ks[1];
-  const __nv_bfloat16* V = static_cast<const __nv_bfloat16*>(a.pool.V) + h * a.pool.vs[1];
-  const __nv_bfloat16* Q = static_cast<const __nv_bfloat16*>(a.Q) + i * a.q_stride + static_cast<int64_t>(hq) * D;
-  float q[PL], o[PL], m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int e = 0; e < PL; ++e) {
-    q[e] = __bfloat162float(Q[lane + 32 * e]);
-    o[e] = 0.f;
-  }
-  for (int64_t j = warp; j < n; j += 4) {
-    const int64_t t = j < sinks ? j : win + j - sinks;
-    const int p = a.table[static_cast<int64_t>(b) * a.max_pages + t / a.pool.page_size];
-    if (p < 0 || p >= a.pool.n_pages) {
-      if (lane == 0) flag_error(a.status, DEVFLAG_BAD_INDEX);
-      continue;
+struct Pa {
+  static constexpr int kTile = D == 256 ? 64 : 128;      // keys per tile
+  static constexpr int kWG = D == 256 ? 1 : 2;           // softmax warpgroups
+  static constexpr int kDB = D / 64;                     // 64-dim blocks of a row
+  static constexpr int kStageBytes = kTile * D * 2;
+  static constexpr int kStages = D == 64 ? 8 : 5;
+  static constexpr int kQBlock = 128 * 128;              // 128 rows x 64 dims
+  static constexpr int kQBytes = kQBlock * kDB;
+  // with the static arrays (3 KB, a multiple of the dynamic array's alignment) all of an SM's shared memory for d = 128
+  static constexpr int kSmem = kWG * kQBytes + kStages * kStageBytes;
+  static constexpr int kSoftmax = kWG * 128;             // softmax threads
+  static constexpr int kThreads = kSoftmax + 96;
+  static constexpr int kPer = (1024 + kThreads - 1) / kThreads;  // sequences per thread in the prologue
+  static constexpr uint32_t kSCols = kTile;              // columns of one S slot (two slots)
+};
+
+struct PaParams {
+  CUtensorMap q, k, v;
+  PagedAttnArgs a;
+  int G, tpt;      // query heads per KV head; tokens per query tile
+  int box, nbox;   // rows of a TMA box; boxes per tile
+  float scale_log2;
+};
+
+// One item: its tokens and the list of its keys.  Place v of the list holds token v below s_al
+// and token v + shift from there on; z0 <= v < z1 and v >= nv are seen by no query.
+struct Item {
+  int tok0, ntok, pf;
+  int s_al, shift, z0, z1, nv, ntiles;
+  bool solo;  // one query tile
+};
+
+template <int D>
+__device__ __forceinline__ Item item_at(const PaParams& p, int nq, int len, int j) {
+  Item it;
+  const int tpi = p.tpt * Pa<D>::kWG;
+  it.tok0 = j * tpi;
+  it.ntok = min(tpi, nq - it.tok0);
+  it.pf = len - nq + it.tok0;
+  const int hi = it.pf + it.ntok;
+  it.s_al = it.shift = it.z0 = it.z1 = 0;
+  if (p.a.window > 0) {
+    const int lo = max(0, it.pf + 1 - p.a.window), lo_al = lo & ~(p.box - 1);
+    it.z0 = min(p.a.n_sinks, lo);
+    const int s_al = (it.z0 + p.box - 1) & ~(p.box - 1);
+    if (s_al < lo_al) {
+      it.s_al = s_al;
+      it.shift = lo_al - s_al;
     }
-    const __nv_bfloat16* kr = K + p * a.pool.ks[0] + (t % a.pool.page_size) * a.pool.ks[2];
-    const __nv_bfloat16* vr = V + p * a.pool.vs[0] + (t % a.pool.page_size) * a.pool.vs[2];
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < PL; ++e) s = fmaf(q[e], __bfloat162float(kr[lane + 32 * e]), s);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
-    s *= a.sm_scale;
-    const float mn = fmaxf(m, s), alpha = expf(m - mn), w = expf(s - mn);
-    l = l * alpha + w;
-    m = mn;
-#pragma unroll
-    for (int e = 0; e < PL; ++e) o[e] = fmaf(w, __bfloat162float(vr[lane + 32 * e]), o[e] * alpha);
+    it.z1 = lo - it.shift;
   }
-  if (lane == 0) m_s[warp] = m, l_s[warp] = l;
+  it.nv = hi - it.shift;
+  it.ntiles = (it.nv + Pa<D>::kTile - 1) / Pa<D>::kTile;
+  it.solo = Pa<D>::kWG == 1 || it.ntok <= p.tpt;
+  return it;
+}
+
+// An item's length on the line: a tile of two query tiles counts twice.
+__device__ __forceinline__ int64_t item_units(const Item& it) {
+  return it.solo ? it.ntiles : 2 * static_cast<int64_t>(it.ntiles);
+}
+
+// The CTAs' cuts of the line and this CTA's first item, written once by the prologue.
+struct Line {
+  int64_t total, seq_start, per_head, start;
+  int nact, b, h, j;
+};
+
+// Walks the pieces of items that fall to this CTA, in order.
+template <int D>
+struct Pieces {
+  const PaParams& p;
+  int64_t u, u0, u1, total, q0_b;
+  int nact, nb, nh, nj, nq_b, len_b;
+  // the current piece
+  Item it;
+  int b, h, t0, t1, c_first, c_last;
+  int64_t q0;
+
+  __device__ Pieces(const PaParams& pp, const Line& s) : p(pp) {
+    total = s.total;
+    nact = s.nact;
+    u0 = blockIdx.x * total / nact;
+    u1 = (blockIdx.x + 1) * total / nact;
+    u = s.start;
+    nb = s.b, nh = s.h, nj = s.j;
+    load();
+  }
+  __device__ void load() {
+    const NewTokens t = new_tokens(p.a.q_begin, p.a.seq_lens, nb,
+                                   static_cast<int64_t>(p.a.max_pages) * p.a.pool.page_size, p.a.n_tokens,
+                                   p.a.max_q_len, nullptr);
+    q0_b = t.q0, nq_b = t.nq, len_b = t.len;
+  }
+  __device__ int owner(int64_t x) const { return static_cast<int>(((x + 1) * nact + total - 1) / total) - 1; }
+  __device__ bool next() {
+    while (u < u1) {
+      it = item_at<D>(p, nq_b, len_b, nj);
+      const int w = it.solo ? 1 : 2;
+      t0 = u >= u0 ? 0 : static_cast<int>((u0 - u + w - 1) / w);
+      t1 = static_cast<int>(min64(it.ntiles, (u1 - u + w - 1) / w));
+      b = nb, h = nh, q0 = q0_b + it.tok0;
+      const bool mine = t0 < t1;
+      if (mine) {
+        c_first = owner(u);
+        c_last = owner(u + static_cast<int64_t>(w) * (it.ntiles - 1));
+      }
+      u += item_units(it);
+      ++nj;
+      if (it.tok0 + it.ntok == nq_b) {
+        nj = 0;
+        if (++nh == p.a.pool.Hkv) {
+          nh = 0;
+          do {
+            if (++nb == p.a.B) break;
+            load();
+          } while (nq_b == 0);
+        }
+      }
+      if (mine) return true;
+    }
+    return false;
+  }
+};
+
+// Places of a piece's loads in the ring: K_0, K_1, V_0, K_2, V_1, ..., V_{n-1}.
+__device__ __forceinline__ int k_place(int i) { return i == 0 ? 0 : 2 * i - 1; }
+__device__ __forceinline__ int v_place(int i, int n) { return i + 1 < n ? 2 * i + 2 : 2 * n - 1; }
+
+struct Waiter {
+  volatile int* dead;
+  int* status;
+  __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+    while (true) {
+      if (mbar_try_wait(bar, parity)) return true;
+      if (*dead) return false;
+      if (global_timer_ns() - t0 > kWaitLimitNs) {
+        flag_error(status, DEVFLAG_TIMEOUT);
+        *dead = 1;
+        return false;
+      }
+    }
+  }
+};
+
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Bits [0, n) of a word, n clamped to [0, 32].
+__device__ __forceinline__ uint32_t bits_below(int n) { return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u); }
+
+// Page of this lane's box of tile i: -2 where the item has no keys, -1 where the table names no page.
+template <int D>
+__device__ __forceinline__ int box_page(const PaParams& p, const Pieces<D>& s, int i, int box, bool on, int* t_out) {
+  const int v = i * Pa<D>::kTile + box * p.box;
+  if (!on || v >= s.it.nv) return -2;
+  const int t = v < s.it.s_al ? v : v + s.it.shift;
+  *t_out = t;
+  const int pg = __ldg(p.a.table + static_cast<int64_t>(s.b) * p.a.max_pages + t / p.a.pool.page_size);
+  return pg < 0 || pg >= p.a.pool.n_pages ? -1 : pg;
+}
+
+// Whether tile i holds rows that no query of the item sees.
+template <int D>
+__device__ __forceinline__ bool edge_tile(const Item& it, int i) {
+  const int v0 = i * Pa<D>::kTile, v1 = v0 + Pa<D>::kTile;
+  return v1 > it.nv || (it.z0 < it.z1 && v0 < it.z1 && v1 > it.z0);
+}
+
+// Stores 32 consecutive outputs of a row.
+template <bool F32>
+__device__ __forceinline__ void store_out32(void* O, int64_t at, const float (&v)[32]) {
+  if constexpr (F32) {
+    float4* o = reinterpret_cast<float4*>(static_cast<float*>(O) + at);
 #pragma unroll
-  for (int e = 0; e < PL; ++e) o_s[warp][lane + 32 * e] = o[e];
+    for (int i = 0; i < 8; ++i) o[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  } else {
+    uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(O) + at);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      o[i] = make_uint4(pack_bf16x2(v[8 * i], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
+                        pack_bf16x2(v[8 * i + 4], v[8 * i + 5]), pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
+  }
+}
+
+template <int D, bool F32>
+__global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __grid_constant__ PaParams p) {
+  using C = Pa<D>;
+  constexpr int kTile = C::kTile, kWG = C::kWG, kDB = C::kDB, kNS = C::kStages;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  __shared__ __align__(8) uint64_t q_full, q_empty, kv_full[kNS], kv_empty[kNS], edge_full[kNS], s_full[2], p_full[2],
+      o_full[2], wg_bar, drain;
+  __shared__ Line line;
+  __shared__ int64_t warp_sum[C::kThreads / 32];
+  __shared__ uint32_t tmem_base_s, bad_s[kPaBadRing];
+  __shared__ float ml_s[2][2][128];  // solo items: each warpgroup's maxima and sums
+  __shared__ int dead_s, last_s;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const PagedAttnArgs& a = p.a;
+  const int64_t cap = static_cast<int64_t>(a.max_pages) * a.pool.page_size;
+
+  // ---- the line: every CTA adds up all sequences' items (a few consecutive ones per thread)
+  int64_t mine = 0, units[C::kPer];
+  const int per = (a.B + C::kThreads - 1) / C::kThreads;
+#pragma unroll
+  for (int e = 0; e < C::kPer; ++e) {
+    units[e] = 0;
+    const int b = tid * per + e;
+    if (e < per && b < a.B) {
+      const NewTokens t = new_tokens(a.q_begin, a.seq_lens, b, cap, a.n_tokens, a.max_q_len,
+                                     blockIdx.x == 0 ? a.status : nullptr);
+      for (int j = 0, at = 0; at < t.nq; ++j) {
+        const Item it = item_at<D>(p, t.nq, t.len, j);
+        units[e] += item_units(it);
+        at += it.ntok;
+      }
+    }
+    mine += units[e] * a.pool.Hkv;
+  }
+  int64_t inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+    if (lane >= o) inc += v;
+  }
+  if (lane == 31) warp_sum[warp] = inc;
   __syncthreads();
-  const float M = fmaxf(fmaxf(m_s[0], m_s[1]), fmaxf(m_s[2], m_s[3]));
-  float L = 0.f, w[4];
+  int64_t before = inc - mine, total = 0;
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    w[u] = M == -INFINITY ? 0.f : expf(m_s[u] - M);
-    L += w[u] * l_s[u];
+  for (int w = 0; w < C::kThreads / 32; ++w) {
+    if (w < warp) before += warp_sum[w];
+    total += warp_sum[w];
   }
-  const int64_t row = i * a.Hq + hq;
-  for (int e = threadIdx.x; e < D; e += 128) {
-    float v = 0.f;
+  // at least two units per CTA, so that each cut piece has a whole tile
+  const int nact = static_cast<int>(min64(gridDim.x, max64(1, total / 2)));
+  if (total == 0 || static_cast<int>(blockIdx.x) >= nact) return;
+  const int64_t u0 = blockIdx.x * total / nact;
+  if (u0 >= before && u0 < before + mine) {
+    int64_t at = before;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) v = fmaf(w[u], o_s[u][e], v);
-    v = L > 0.f ? v / L : 0.f;
-    if (a.out_bf16) static_cast<__nv_bfloat16*>(a.O)[row * D + e] = __float2bfloat16_rn(v);
-    else static_cast<float*>(a.O)[row * D + e] = v;
+    for (int e = 0; e < C::kPer; ++e) {
+      const int64_t n = units[e] * a.pool.Hkv;
+      if (u0 >= at && u0 < at + n) {
+        line.b = tid * per + e;
+        line.seq_start = at;
+        line.per_head = units[e];
+      }
+      at += n;
+    }
+    line.total = total;
+    line.nact = nact;
   }
-  if (a.lse && threadIdx.x == 0) a.lse[row] = L > 0.f ? M + logf(L) : -INFINITY;
+  if (tid == 0) {
+    dead_s = 0;
+    mbar_init(&q_full, 1);
+    mbar_init(&q_empty, 1);
+    for (int i = 0; i < kNS; ++i) {
+      mbar_init(&kv_full[i], 1);
+      mbar_init(&kv_empty[i], 1);
+      mbar_init(&edge_full[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 128);
+      mbar_init(&o_full[i], 1);
+    }
+    mbar_init(&wg_bar, C::kSoftmax);
+    mbar_init(&drain, 1);
+    fence_mbarrier_init();
+  }
+  constexpr int kMmaWarp = kWG * 4, kLoadWarp = kMmaWarp + 1, kZeroWarp = kMmaWarp + 2;
+  if (warp == kMmaWarp) tmem_alloc(&tmem_base_s, kTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 0) {  // this CTA's first item within its sequence
+    const NewTokens t = new_tokens(a.q_begin, a.seq_lens, line.b, cap, a.n_tokens, a.max_q_len, nullptr);
+    int64_t rem = u0 - line.seq_start;
+    const int h = static_cast<int>(rem / line.per_head);
+    rem -= h * line.per_head;
+    int64_t at = u0 - rem;
+    const int tpi = p.tpt * kWG;
+    for (int j0 = 0; j0 * static_cast<int64_t>(tpi) < t.nq; j0 += 32) {
+      const int j = j0 + lane;
+      const int64_t n = j * static_cast<int64_t>(tpi) < t.nq ? item_units(item_at<D>(p, t.nq, t.len, j)) : 0;
+      int64_t s = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xFFFFFFFFu, s, o);
+        if (lane >= o) s += v;
+      }
+      const int64_t all = __shfl_sync(0xFFFFFFFFu, s, 31);
+      if (rem < all) {
+        if (rem >= s - n && rem < s) {
+          line.h = h;
+          line.j = j;
+          line.start = at + s - n;
+        }
+        break;
+      }
+      rem -= all;
+      at += all;
+    }
+  }
+  __syncthreads();
+
+  const uint32_t tmem = tmem_base_s;
+  const uint32_t base = smem_u32(smem_raw);
+  const uint32_t q_s = base, kv_s = base + kWG * C::kQBytes;
+  const Waiter wait{&dead_s, a.status};
+  Pieces<D> s(p, line);
+
+  if (warp == kLoadWarp) {
+    // ------------------------------------------------------------------ loads
+    const int box = lane / kDB, db = lane % kDB;
+    const bool on = box < p.nbox;
+    uint32_t n = 0, tiles = 0;  // ring places filled; tiles begun
+    bool ok = true;
+    for (int piece = 0; ok && s.next(); ++piece) {
+      if (piece > 0) ok = __all_sync(0xFFFFFFFFu, wait(&q_empty, (piece - 1) & 1));
+      if (!ok) break;
+      const int nqt = s.it.solo ? 1 : 2;
+      if (lane == 0) mbar_arrive_expect_tx(&q_full, nqt * kDB * p.tpt * p.G * 128);
+      __syncwarp();
+      if (lane < nqt * kDB)
+        tma_load_3d(q_s + (lane / kDB) * C::kQBytes + db * C::kQBlock, &p.q, db * 64, s.h * p.G,
+                    static_cast<int>(s.q0) + (lane / kDB) * p.tpt, &q_full);
+      int t_next = 0, t_prev = 0, pg_prev = -2;
+      int pg_next = box_page<D>(p, s, s.t0, box, on, &t_next);
+      // step i: K of tile i, V of tile i - 1
+      for (int i = s.t0; ok && i <= s.t1; ++i) {
+        const int pg = pg_next, t = t_next;
+        pg_next = -2;
+        if (i + 1 < s.t1) pg_next = box_page<D>(p, s, i + 1, box, on, &t_next);
+        for (int kv = 0; kv < 2; ++kv) {
+          const bool is_v = kv == 1;
+          if (is_v ? i == s.t0 : i == s.t1) continue;
+          const int pgx = is_v ? pg_prev : pg, tx = is_v ? t_prev : t;
+          const uint32_t st = n % kNS;
+          if (n >= kNS) ok = __all_sync(0xFFFFFFFFu, wait(&kv_empty[st], ((n / kNS) & 1) ^ 1));
+          if (!ok) break;
+          const uint32_t bad = __ballot_sync(0xFFFFFFFFu, pgx == -1);
+          const uint32_t loads = __popc(__ballot_sync(0xFFFFFFFFu, pgx >= 0));
+          uint64_t* bar = &kv_full[st];
+          if (is_v && (bad || edge_tile<D>(s.it, i - 1))) bar = &edge_full[st];
+          if (lane == 0) {
+            if (!is_v) {
+              bad_s[tiles % kPaBadRing] = bad;
+              if (bad) flag_error(a.status, DEVFLAG_BAD_INDEX);
+            }
+            mbar_arrive_expect_tx(bar, loads * p.box * 128);
+          }
+          if (!is_v) ++tiles;
+          __syncwarp();
+          if (pgx >= 0)
+            tma_load_4d(kv_s + st * C::kStageBytes + db * (kTile * 128) + box * p.box * 128, is_v ? &p.v : &p.k,
+                        db * 64, tx % a.pool.page_size, s.h, pgx, bar);
+          ++n;
+        }
+        pg_prev = pg;
+        t_prev = t;
+      }
+    }
+    if (!ok) {  // wait for the copies in flight
+      if (lane == 0)
+        for (uint32_t i = n > kNS ? n - kNS : 0; i < n; ++i)
+          mbar_wait_bounded(&kv_full[i % kNS], (i / kNS) & 1, a.status);
+    }
+  } else if (warp == kZeroWarp) {
+    // ------------------------------------------------------------------ unseen V rows
+    const int box = lane / kDB;
+    const bool on = box < p.nbox;
+    uint32_t n0 = 0, par = 0;  // ring place of the piece; phase of each edge barrier
+    bool ok = true;
+    while (ok && s.next()) {
+      const int nt = s.t1 - s.t0;
+      for (int i = s.t0; ok && i < s.t1; ++i) {
+        int t = 0;
+        const uint32_t bad = __ballot_sync(0xFFFFFFFFu, box_page<D>(p, s, i, box, on, &t) == -1);
+        if (!bad && !edge_tile<D>(s.it, i)) continue;
+        const uint32_t st = (n0 + v_place(i - s.t0, nt)) % kNS;
+        ok = __all_sync(0xFFFFFFFFu, wait(&edge_full[st], (par >> st) & 1));
+        if (!ok) break;
+        par ^= 1u << st;
+        for (int r = lane; r < kTile; r += 32) {
+          const int v = i * kTile + r;
+          const bool lost = (bad >> ((r / p.box) * kDB)) & 1;
+          if (lost || v >= s.it.nv || (v >= s.it.z0 && v < s.it.z1)) {
+#pragma unroll
+            for (int x = 0; x < kDB * 8; ++x)
+              st_shared_v4(kv_s + st * C::kStageBytes + (x >> 3) * (kTile * 128) + r * 128 + (x & 7) * 16, 0, 0, 0, 0);
+          }
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&kv_full[st]);
+      }
+      n0 += 2 * nt;
+    }
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------------ MMAs
+    if (lane == 0) {
+      const uint32_t idesc_s = instr_desc(128, kTile, false, false);
+      const uint32_t idesc_o = instr_desc(128, D, true, false);
+      uint32_t n0 = 0, np[2] = {0, 0};
+      bool ok = true;
+      auto full = [&](uint32_t place) { return wait(&kv_full[place % kNS], (place / kNS) & 1); };
+      auto scores = [&](int slot, int qt, uint32_t place) {
+        const uint32_t qa = q_s + qt * C::kQBytes, ka = kv_s + (place % kNS) * C::kStageBytes;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          umma_bf16(tmem + slot * C::kSCols, smem_desc(qa + (kk >> 2) * C::kQBlock + (kk & 3) * 32, 16, 1024),
+                    smem_desc(ka + (kk >> 2) * (kTile * 128) + (kk & 3) * 32, 16, 1024), idesc_s, kk != 0);
+      };
+      auto values = [&](int slot, int o, uint32_t place, bool first) {
+        const uint32_t va = kv_s + (place % kNS) * C::kStageBytes;
+#pragma unroll
+        for (int part = 0; part < (F32 ? 2 : 1); ++part)
+#pragma unroll
+          for (int kt = 0; kt < kTile / 16; ++kt)
+            umma_bf16_ts(tmem + kPaOCol + o * D, tmem + slot * C::kSCols + part * (kTile / 2) + kt * 8,
+                         smem_desc(va + kt * 2048, kTile * 128, 1024), idesc_o, !first || part || kt);
+      };
+      for (int piece = 0; ok && s.next(); ++piece) {
+        const int n = s.t1 - s.t0;
+        const bool pair = !s.it.solo;
+        ok = wait(&q_full, piece & 1) && full(n0);
+        if (!ok) break;
+        tc_fence_after();
+        for (int st = 0; st < (pair ? 2 : 1); ++st) {
+          scores(st, st, n0);
+          umma_commit(&s_full[st]);
+        }
+        umma_commit(&kv_empty[n0 % kNS]);
+        if (n == 1) umma_commit(&q_empty);
+        if (!pair && n > 1) {
+          ok = full(n0 + k_place(1));
+          if (!ok) break;
+          scores(1, 0, n0 + k_place(1));
+          umma_commit(&s_full[1]);
+          umma_commit(&kv_empty[(n0 + k_place(1)) % kNS]);
+          if (n == 2) umma_commit(&q_empty);
+        }
+        for (int i = 0; ok && i < n; ++i) {
+          const uint32_t vp = n0 + v_place(i, n);
+          if (pair) {
+            const uint32_t kp = n0 + k_place(i + 1);
+            ok = (i + 1 == n || full(kp)) && full(vp);
+            for (int st = 0; ok && st < 2; ++st) {
+              ok = wait(&p_full[st], np[st]++ & 1);
+              if (!ok) break;
+              tc_fence_after();
+              values(st, st, vp, i == 0);
+              if (st == 1) umma_commit(&kv_empty[vp % kNS]);
+              umma_commit(&o_full[st]);
+              if (i + 1 < n) {
+                scores(st, st, kp);
+                if (st == 1) {
+                  umma_commit(&kv_empty[kp % kNS]);
+                  if (i + 2 == n) umma_commit(&q_empty);
+                }
+                umma_commit(&s_full[st]);
+              }
+            }
+          } else {
+            const int slot = i & 1, o = kWG == 2 ? slot : 0;
+            ok = full(vp) && wait(&p_full[slot], np[slot]++ & 1);
+            if (!ok) break;
+            tc_fence_after();
+            values(slot, o, vp, i == 0 || (kWG == 2 && i == 1));
+            umma_commit(&kv_empty[vp % kNS]);
+            umma_commit(&o_full[slot]);
+            if (i + 2 < n) {
+              const uint32_t kp = n0 + k_place(i + 2);
+              ok = full(kp);
+              if (!ok) break;
+              scores(slot, 0, kp);
+              umma_commit(&kv_empty[kp % kNS]);
+              if (i + 3 == n) umma_commit(&q_empty);
+              umma_commit(&s_full[slot]);
+            }
+          }
+        }
+        n0 += 2 * n;
+      }
+      umma_commit(&drain);  // every MMA and commit before it, in the error case too
+      mbar_wait_bounded(&drain, 0, a.status);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------------ softmax and output
+    const int wg = warp >> 2, quad = warp & 3;
+    const int r = quad * 32 + lane, tr = r / p.G;
+    const int rows_tile = p.tpt * p.G;
+    const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    uint32_t ns[2] = {0, 0}, no[2] = {0, 0}, tiles0 = 0, nwg = 0;  // barrier phases; tiles before the piece
+    bool ok = true;
+    auto all_ok = [&](bool x) { return __all_sync(0xFFFFFFFFu, x) != 0; };
+    auto sync_wgs = [&]() {
+      mbar_arrive(&wg_bar);
+      return all_ok(wait(&wg_bar, nwg++ & 1));
+    };
+    while (ok && s.next()) {
+      const bool solo = s.it.solo;
+      const int qoff = !solo && wg == 1 ? p.tpt : 0;
+      const bool valid = r < rows_tile && qoff + tr < s.it.ntok;
+      const bool active = __any_sync(0xFFFFFFFFu, valid);
+      const int pos = s.it.pf + min(qoff + tr, s.it.ntok - 1), pl = s.it.pf + s.it.ntok - 1;
+      // this row sees places [0, va) and [vb, vc) of the list; all rows see [b_max, c_min)
+      const int W = a.window;
+      const int va = W > 0 ? min(a.n_sinks, pos + 1) : 0;
+      const int vb = (W > 0 ? max(0, pos + 1 - W) : 0) - s.it.shift, vc = pos + 1 - s.it.shift;
+      const int b_max = (W > 0 ? max(0, pl + 1 - W) : 0) - s.it.shift, c_min = s.it.pf + 1 - s.it.shift;
+      const bool split_keys = kWG == 2 && solo;
+      const int o_slot = kWG == 2 ? wg : 0;
+      float m = -INFINITY, l = 0.f;
+      bool first = true;
+      int prev = 0;  // slot of the tile before: a barrier per slot, since with one warpgroup two products may be under way
+      for (int i = s.t0 + (split_keys ? wg : 0); i < s.t1; i += split_keys ? 2 : 1) {
+        const int slot = kWG == 2 ? wg : ((i - s.t0) & 1);
+        ok = all_ok(wait(&s_full[slot], ns[slot]++ & 1));
+        if (!ok) break;
+        tc_fence_after();
+        if (active) {
+          float x[kTile];
+          if constexpr (kTile == 128) tmem_ld128(trow + slot * C::kSCols, x);
+          else tmem_ld64(trow + slot * C::kSCols, x);
+          const int v0 = i * kTile;
+          const uint32_t bad = bad_s[(tiles0 + i - s.t0) % kPaBadRing];
+          if (bad || v0 < b_max || v0 + kTile > c_min) {
+#pragma unroll
+            for (int c = 0; c < kTile / 32; ++c) {
+              const int at = v0 + 32 * c;
+              uint32_t w = bits_below(va - at) | (bits_below(vc - at) & ~bits_below(vb - at));
+              if (bad)
+                for (int k = 0; k < p.nbox; ++k)
+                  if ((bad >> (k * kDB)) & 1)
+                    w &= ~(bits_below((k + 1) * p.box - 32 * c) & ~bits_below(k * p.box - 32 * c));
+#pragma unroll
+              for (int e = 0; e < 32; ++e) x[32 * c + e] = (w >> e) & 1 ? x[32 * c + e] : -INFINITY;
+            }
+          }
+          float mx0 = x[0], mx1 = x[1], mx2 = x[2], mx3 = x[3];
+#pragma unroll
+          for (int e = 4; e < kTile; e += 4) {
+            mx0 = fmaxf(mx0, x[e]);
+            mx1 = fmaxf(mx1, x[e + 1]);
+            mx2 = fmaxf(mx2, x[e + 2]);
+            mx3 = fmaxf(mx3, x[e + 3]);
+          }
+          const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
+          const bool move = m == -INFINITY ? mx > -INFINITY : (mx - m) * p.scale_log2 > kPaRescale;
+          if (__any_sync(0xFFFFFFFFu, move)) {
+            float alpha = 1.f;
+            if (move) {
+              alpha = m == -INFINITY ? 0.f : exp2_approx((m - mx) * p.scale_log2);
+              m = mx;
+              l *= alpha;
+            }
+            if (!first) {  // the products before this tile have to be done
+              ok = all_ok(wait(&o_full[prev], (no[prev] - 1) & 1));
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll 1
+              for (int c = 0; c < D / 32; ++c) {
+                float v[32];
+                tmem_ld32(trow + kPaOCol + o_slot * D + 32 * c, v);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] *= alpha;
+                tmem_st32(trow + kPaOCol + o_slot * D + 32 * c, v);
+              }
+            }
+          }
+          const float mm = m == -INFINITY ? 0.f : m * p.scale_log2;
+          float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+          for (int c = 0; c < kTile / 32; ++c) {
+            uint32_t hi[16], lo[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float p0 = exp2_approx(fmaf(x[32 * c + 2 * e], p.scale_log2, -mm));
+              const float p1 = exp2_approx(fmaf(x[32 * c + 2 * e + 1], p.scale_log2, -mm));
+              l0 += p0;
+              l1 += p1;
+              hi[e] = pack_bf16x2(p0, p1);
+              if constexpr (F32)
+                lo[e] = pack_bf16x2(p0 - bf16_bits_to_float(hi[e] & 0xFFFFu), p1 - __uint_as_float(hi[e] & 0xFFFF0000u));
+            }
+            tmem_st16_nowait(trow + slot * C::kSCols + 16 * c, hi);
+            if constexpr (F32) tmem_st16_nowait(trow + slot * C::kSCols + kTile / 2 + 16 * c, lo);
+          }
+          l += l0 + l1;
+          tmem_st_wait();
+        }
+        first = false;
+        ++no[slot];
+        prev = slot;
+        tc_fence_before();
+        mbar_arrive(&p_full[slot]);
+      }
+      tiles0 += s.t1 - s.t0;
+      if (!ok) break;
+      if (!first) {
+        ok = all_ok(wait(&o_full[prev], (no[prev] - 1) & 1));
+        if (!ok) break;
+      }
+      // the row's factor on each accumulator that holds a share of it
+      float f0 = 1.f, f1 = 0.f;
+      if (split_keys) {
+        ml_s[wg][0][r] = m;
+        ml_s[wg][1][r] = l;
+        ok = sync_wgs();
+        if (!ok) break;
+        const float m0 = ml_s[0][0][r], m1 = ml_s[1][0][r], l0 = ml_s[0][1][r], l1 = ml_s[1][1][r];
+        m = fmaxf(m0, m1);
+        f0 = l0 > 0.f ? exp2_approx((m0 - m) * p.scale_log2) : 0.f;
+        f1 = l1 > 0.f ? exp2_approx((m1 - m) * p.scale_log2) : 0.f;
+        l = f0 * l0 + f1 * l1;
+      }
+      tc_fence_after();
+      const bool whole = s.c_first == s.c_last;
+      const int row = (solo ? 0 : wg * rows_tile) + r;  // within the item
+      const int64_t orow = (s.q0 + row / p.G) * a.Hq + s.h * p.G + row % p.G;
+      const int slot_out = 2 * static_cast<int>(blockIdx.x) + (static_cast<int>(blockIdx.x) == s.c_first ? 1 : 0);
+      const int64_t prow = static_cast<int64_t>(slot_out) * a.rows_cap + row;
+      if (active) {
+        const float g = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
+        const int c0 = split_keys ? wg * (D / 64) : 0, c1 = split_keys ? c0 + D / 64 : D / 32;
+#pragma unroll 1
+        for (int c = c0; c < c1; ++c) {
+          float v[32];
+          if (split_keys) {
+            float y[32];
+            tmem_ld32(trow + kPaOCol + 32 * c, v);
+            tmem_ld32(trow + kPaOCol + D + 32 * c, y);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = (f0 != 0.f ? f0 * v[e] : 0.f) + (f1 != 0.f ? f1 * y[e] : 0.f);
+          } else {
+            tmem_ld32(trow + kPaOCol + o_slot * D + 32 * c, v);
+          }
+          if (valid) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] *= g;
+            if (whole) store_out32<F32>(a.O, orow * D + 32 * c, v);
+            else store_out32<true>(a.part_o, prow * D + 32 * c, v);
+          }
+          __syncwarp();
+        }
+        if (valid && !(split_keys && wg == 1)) {
+          if (!whole) a.part_ml[prow] = make_float2(m, l);
+          else if (a.lse) a.lse[orow] = l > 0.f ? m * a.sm_scale + logf(l) : -INFINITY;
+        }
+      }
+      tc_fence_before();
+      if (whole) {
+        if (split_keys) ok = sync_wgs();  // neither accumulator is overwritten before both have read it
+        continue;
+      }
+      // ---- the last CTA of a cut item merges its pieces
+      __threadfence();
+      ok = sync_wgs();
+      if (!ok) break;
+      if (tid == 0) {
+        const int n = s.c_last - s.c_first + 1;
+        const bool last = atomicAdd(a.counters + s.c_first, 1) == n - 1;
+        if (last) a.counters[s.c_first] = 0;
+        __threadfence();
+        last_s = last;
+      }
+      ok = sync_wgs();
+      if (!ok) break;
+      if (last_s) {
+        __threadfence();
+        const int n = s.c_last - s.c_first + 1;
+        const int rows = s.it.ntok * p.G;
+        for (int idx = tid; idx < rows * (D / 4); idx += C::kSoftmax) {
+          const int rr = idx / (D / 4), c = idx % (D / 4);
+          auto at = [&](int k) {
+            return static_cast<int64_t>(2 * (s.c_first + k) + (k == 0 ? 1 : 0)) * a.rows_cap + rr;
+          };
+          float M = -INFINITY, L = 0.f;
+          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+          for (int k = 0; k < n; ++k) M = fmaxf(M, __ldcg(&a.part_ml[at(k)].x));
+#pragma unroll 4
+          for (int k = 0; k < n; ++k) {
+            const float2 ml = __ldcg(&a.part_ml[at(k)]);
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + at(k) * D) + c);
+            const float w = ml.y > 0.f ? exp2_approx((ml.x - M) * p.scale_log2) : 0.f;
+            L = fmaf(w, ml.y, L);
+            o.x = fmaf(w, v.x, o.x), o.y = fmaf(w, v.y, o.y), o.z = fmaf(w, v.z, o.z), o.w = fmaf(w, v.w, o.w);
+          }
+          const float g = L > 0.f ? 1.f / L : 0.f;
+          o.x *= g, o.y *= g, o.z *= g, o.w *= g;
+          const int64_t to = (s.q0 + rr / p.G) * a.Hq + s.h * p.G + rr % p.G;
+          if constexpr (F32)
+            reinterpret_cast<float4*>(static_cast<float*>(a.O) + to * D)[c] = o;
+          else
+            reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.O) + to * D)[c] =
+                make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+          if (c == 0 && a.lse) a.lse[to] = L > 0.f ? M * a.sm_scale + logf(L) : -INFINITY;
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// ------------------------------------------------------------------ host
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+  static EncodeTiled fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess)
+      return static_cast<EncodeTiled>(nullptr);
+    return reinterpret_cast<EncodeTiled>(f);
+  }();
+  return fn;
+}
+
+// Map of a bf16 tensor whose innermost extent is d (boxes of 64 of them, 128-byte swizzle).  The
+// stride of an extent of 1 is never used and set to a row's, which the encoder accepts.
+bool encode(CUtensorMap* m, const void* base, int rank, const int64_t* extent, const int64_t* stride, const int* box) {
+  cuuint64_t dims[4], strides[3];
+  cuuint32_t boxes[4], ones[4] = {1, 1, 1, 1};
+  for (int i = 0; i < rank; ++i) {
+    dims[i] = static_cast<cuuint64_t>(extent[i]);
+    boxes[i] = static_cast<cuuint32_t>(box[i]);
+    if (i > 0) strides[i - 1] = static_cast<cuuint64_t>(extent[i] > 1 ? stride[i] : extent[0]) * 2;
+  }
+  const EncodeTiled fn = encode_tiled();
+  return fn && fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank), const_cast<void*>(base), dims,
+                  strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool F32>
+cudaError_t launch(const PagedAttnArgs& a, int num_sms, cudaStream_t s) {
+  using C = Pa<D>;
+  PaParams p;
+  p.a = a;
+  p.G = a.Hq / a.pool.Hkv;
+  p.tpt = paged_attn_tile_tokens(p.G);
+  p.box = 16;  // the largest power of two that divides a page, at most a tile
+  while (p.box < C::kTile && a.pool.page_size % (2 * p.box) == 0) p.box *= 2;
+  p.nbox = C::kTile / p.box;
+  p.scale_log2 = a.sm_scale * kLog2e;
+  const int64_t qe[3] = {D, a.Hq, a.n_tokens}, qs[3] = {1, D, a.q_stride};
+  const int qb[3] = {64, p.G, p.tpt};
+  const int64_t ke[4] = {D, a.pool.page_size, a.pool.Hkv, a.pool.n_pages};
+  const int64_t ks[4] = {1, a.pool.ks[2], a.pool.ks[1], a.pool.ks[0]};
+  const int64_t vs[4] = {1, a.pool.vs[2], a.pool.vs[1], a.pool.vs[0]};
+  const int kb[4] = {64, p.box, 1, 1};
+  if (!encode(&p.q, a.Q, 3, qe, qs, qb) || !encode(&p.k, a.pool.K, 4, ke, ks, kb) ||
+      !encode(&p.v, a.pool.V, 4, ke, vs, kb))
+    return cudaErrorInvalidValue;
+  auto kernel = paged_attn_kernel<D, F32>;
+  static int done[64] = {0};
+  const cudaError_t e = set_smem_limit_once(kernel, C::kSmem, done);
+  if (e != cudaSuccess) return e;
+  return launch_ex(kernel, dim3(num_sms), dim3(C::kThreads), C::kSmem, s, 0, p);
 }
 
 }  // namespace
 
+int paged_attn_tile_tokens(int G) { return 128 / G; }
+
+int paged_attn_rows(int d, int G, int64_t max_q_len) {
+  const int64_t item = static_cast<int64_t>(paged_attn_tile_tokens(G)) * (d == 256 ? 1 : 2);
+  return static_cast<int>(min64(item, max_q_len)) * G;
+}
+
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, int num_sms, cudaStream_t s) {
-  (void)num_sms;
-  const dim3 grid(static_cast<unsigned>(a.n_tokens), a.Hq);
   switch (a.pool.d) {
-    case 64: return launch_ex(paged_attn_simple_kernel<64>, grid, dim3(128), 0, s, 0, a);
-    case 128: return launch_ex(paged_attn_simple_kernel<128>, grid, dim3(128), 0, s, 0, a);
-    case 256: return launch_ex(paged_attn_simple_kernel<256>, grid, dim3(128), 0, s, 0, a);
+    case 64: return a.out_bf16 ? launch<64, false>(a, num_sms, s) : launch<64, true>(a, num_sms, s);
+    case 128: return a.out_bf16 ? launch<128, false>(a, num_sms, s) : launch<128, true>(a, num_sms, s);
+    case 256: return a.out_bf16 ? launch<256, false>(a, num_sms, s) : launch<256, true>(a, num_sms, s);
   }
   return cudaErrorNotSupported;
 }
