@@ -10,7 +10,7 @@ import ctypes as C
 import torch
 
 from . import _binding as _b
-from ._binding import OUT_BF16, OUT_F32, _check, _stream, load, workspace_init
+from ._binding import OUT_BF16, OUT_F32, _check, load, workspace_init
 
 
 class PagedLayout(C.Structure):
@@ -38,52 +38,78 @@ def _signatures():
 _b.SIGNATURE_SOURCES.append(_signatures)
 
 
-def _dev(t, what):
+# A decode step makes several of these calls, each on a few microseconds of GPU work, so the checks
+# below read every property of a tensor once and leave the wording of a refusal to _refuse().
+def _refuse(t, what, dev, expected):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{what}: device tensor expected")
-    if t.device.index != torch.cuda.current_device():
+    if t.get_device() != dev:
         raise ValueError(f"{what} is on {t.device}, not on the current device")
-    return t
+    raise ValueError(f"{what}: {expected} expected, got {t.dtype} {tuple(t.shape)} with strides {t.stride()}")
 
 
-def _i32(t, shape, what):
-    """Pointer of a contiguous int32 device tensor of the given shape (-1: any length)."""
-    _dev(t, what)
-    if t.dtype != torch.int32 or t.dim() != len(shape) or any(w not in (-1, n) for w, n in zip(shape, t.shape)):
-        raise ValueError(f"{what}: int32 tensor of shape {tuple(shape)} expected, got {t.dtype} {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{what}: contiguous tensor expected")
+def _device():
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else 0
+
+
+def _stream(stream, dev):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return _b._stream(stream)
+
+
+def _packed(t, dtype, shape, what, dev):
+    """Pointer of a contiguous device tensor of the given type and shape."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype is not dtype or t.shape != shape or \
+            not t.is_contiguous():
+        _refuse(t, what, dev, f"contiguous {dtype} tensor of shape {shape}")
     return t.data_ptr()
 
 
-def _pool(L, t, strides, what):
-    _dev(t, what)
-    if t.dtype != torch.bfloat16 or tuple(t.shape) != (L.n_pages, L.Hkv, L.page_size, L.d) or t.stride(3) != 1:
-        raise ValueError(f"{what}: bfloat16 pool [n_pages, Hkv, page_size, d] of the layout expected")
-    if any(n > 1 and a != b for n, a, b in zip(t.shape, t.stride(), strides)):
-        raise ValueError(f"{what}: strides {t.stride()} differ from the layout's")
-    return t.data_ptr()
+def _list(t, what, dev):
+    """(pointer, length) of a contiguous int32 device tensor of one dimension."""
+    n = t.numel() if isinstance(t, torch.Tensor) else 0
+    return _packed(t, torch.int32, (n,), what, dev), n
 
 
-def _rows(t, heads, d, what):
-    """(pointer, row stride) of packed token rows [n, heads, d], each row's heads contiguous."""
-    _dev(t, what)
-    if t.dtype != torch.bfloat16 or t.dim() != 3 or tuple(t.shape[1:]) != (heads, d):
-        raise ValueError(f"{what}: bfloat16 rows [n, {heads}, {d}] expected, got {t.dtype} {tuple(t.shape)}")
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
-        raise ValueError(f"{what}: the heads of a row must be contiguous")
-    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else heads * d)
+def _pools(L, K, V, dev):
+    shape = (L.n_pages, L.Hkv, L.page_size, L.d)
+    for t, strides, what in ((K, L.k_stride[:], "K"), (V, L.v_stride[:], "V")):
+        if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype is not torch.bfloat16 or \
+                t.shape != shape:
+            _refuse(t, what, dev, f"bfloat16 pool {shape}")
+        a, b, c, one = t.stride()
+        if one != 1 or [a, b, c] != strides and any(n > 1 and x != y for n, x, y in zip(shape, (a, b, c), strides)):
+            _refuse(t, what, dev, f"the layout's strides {strides}")
+    return K.data_ptr(), V.data_ptr()
 
 
-def _ws(ws):
+def _rows(t, heads, d, what, dev):
+    """(pointer, rows, row stride) of packed token rows [n, heads, d], each row's heads contiguous."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype is not torch.bfloat16 or t.dim() != 3:
+        _refuse(t, what, dev, f"bfloat16 rows [n, {heads}, {d}]")
+    n, h, e = t.shape
+    row, head, one = t.stride()
+    if h != heads or e != d or one != 1 or (head != d and heads > 1):
+        _refuse(t, what, dev, f"bfloat16 rows [n, {heads}, {d}], the heads of a row contiguous,")
+    return t.data_ptr(), n, (row if n > 1 else heads * d)
+
+
+def _table(L, page_table, dev):
+    return _packed(page_table, torch.int32, (L.B, L.max_pages), "page_table", dev)
+
+
+def _book(L, page_table, ref_count, seq_lens, dev):
+    return (_table(L, page_table, dev), _packed(ref_count, torch.int32, (L.n_pages,), "ref_count", dev),
+            _packed(seq_lens, torch.int32, (L.B,), "seq_lens", dev))
+
+
+def _ws(ws, dev):
     if ws is None:
         return None, 0
-    return _dev(ws, "ws").data_ptr(), ws.numel() * ws.element_size()
-
-
-def _book(L, page_table, ref_count, seq_lens):
-    return (_i32(page_table, (L.B, L.max_pages), "page_table"), _i32(ref_count, (L.n_pages,), "ref_count"),
-            _i32(seq_lens, (L.B,), "seq_lens"))
+    if not isinstance(ws, torch.Tensor) or ws.get_device() != dev:
+        _refuse(ws, "ws", dev, "workspace")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def make_paged_layout(K: torch.Tensor, V: torch.Tensor, page_table: torch.Tensor, Hq: int,
@@ -118,82 +144,84 @@ def alloc_paged_workspace(L: PagedLayout, max_q_len: int = 0, device=None) -> to
 
 def paged_append_kv(L, K_new, V_new, K, V, page_table, q_begin, seq_lens, ws, stream=None):
     """Write the newest tokens' rows K_new, V_new [n_tokens, Hkv, d] into their pages."""
-    k, ks = _rows(K_new, L.Hkv, L.d, "K_new")
-    v, vs = _rows(V_new, L.Hkv, L.d, "V_new")
-    if K_new.shape[0] != V_new.shape[0] or ks != vs:
+    dev, H, d, B = _device(), L.Hkv, L.d, L.B
+    k, nk, ks = _rows(K_new, H, d, "K_new", dev)
+    v, nv, vs = _rows(V_new, H, d, "V_new", dev)
+    if nk != nv or ks != vs:
         raise ValueError("K_new and V_new must have the same rows and row stride")
-    w, n = _ws(ws)
-    _check("jssa_paged_append_kv", load().jssa_paged_append_kv(
-        C.byref(L), k, v, ks, K_new.shape[0], _pool(L, K, L.k_stride, "K"), _pool(L, V, L.v_stride, "V"),
-        _i32(page_table, (L.B, L.max_pages), "page_table"), _i32(q_begin, (L.B + 1,), "q_begin"),
-        _i32(seq_lens, (L.B,), "seq_lens"), w, n, _stream(stream)))
+    code = load().jssa_paged_append_kv(
+        C.byref(L), k, v, ks, nk, *_pools(L, K, V, dev), _table(L, page_table, dev),
+        _packed(q_begin, torch.int32, (B + 1,), "q_begin", dev), _packed(seq_lens, torch.int32, (B,), "seq_lens", dev),
+        *_ws(ws, dev), _stream(stream, dev))
+    _check("jssa_paged_append_kv", code)
 
 
 def paged_attn(L, Q, K, V, page_table, q_begin, max_q_len: int, seq_lens, window: int, n_sinks: int, sm_scale: float,
                O, lse=None, ws=None, stream=None):
     """Causal attention of the newest tokens Q [n_tokens, Hq, d] over their sequences' pages, with
     an optional sliding window (window > 0) and n_sinks first tokens that stay visible."""
-    q, qs = _rows(Q, L.Hq, L.d, "Q")
-    rows = (Q.shape[0], L.Hq)
-    _dev(O, "O")
-    if tuple(O.shape) != rows + (L.d,) or not O.is_contiguous() or \
-            O.dtype != (torch.bfloat16 if L.out_dtype == OUT_BF16 else torch.float32):
-        raise ValueError("O: contiguous [n_tokens, Hq, d] of the layout's output type expected")
-    if lse is not None:
-        _dev(lse, "lse")
-        if tuple(lse.shape) != rows or not lse.is_contiguous() or lse.dtype != torch.float32:
-            raise ValueError("lse: contiguous float32 [n_tokens, Hq] expected")
-    w, n = _ws(ws)
-    _check("jssa_paged_attn", load().jssa_paged_attn(
-        C.byref(L), q, qs, Q.shape[0], max_q_len, _pool(L, K, L.k_stride, "K"), _pool(L, V, L.v_stride, "V"),
-        _i32(page_table, (L.B, L.max_pages), "page_table"), _i32(q_begin, (L.B + 1,), "q_begin"),
-        _i32(seq_lens, (L.B,), "seq_lens"), window, n_sinks, sm_scale, O.data_ptr(),
-        lse.data_ptr() if lse is not None else None, w, n, _stream(stream)))
+    dev, Hq, d, B = _device(), L.Hq, L.d, L.B
+    q, n, qs = _rows(Q, Hq, d, "Q", dev)
+    code = load().jssa_paged_attn(
+        C.byref(L), q, qs, n, max_q_len, *_pools(L, K, V, dev), _table(L, page_table, dev),
+        _packed(q_begin, torch.int32, (B + 1,), "q_begin", dev), _packed(seq_lens, torch.int32, (B,), "seq_lens", dev),
+        window, n_sinks, sm_scale,
+        _packed(O, torch.bfloat16 if L.out_dtype == OUT_BF16 else torch.float32, (n, Hq, d), "O", dev),
+        None if lse is None else _packed(lse, torch.float32, (n, Hq), "lse", dev), *_ws(ws, dev),
+        _stream(stream, dev))
+    _check("jssa_paged_attn", code)
 
 
 def pages_fork(L, src, dst, page_table, ref_count, seq_lens, ws, stream=None):
     """Sequence dst[i] (empty) becomes a copy of sequence src[i] that shares its pages."""
-    s = _i32(src, (-1,), "src")
-    w, n = _ws(ws)
-    _check("jssa_pages_fork", load().jssa_pages_fork(
-        C.byref(L), s, _i32(dst, (src.shape[0],), "dst"), src.shape[0], *_book(L, page_table, ref_count, seq_lens),
-        w, n, _stream(stream)))
+    dev = _device()
+    s, n = _list(src, "src", dev)
+    code = load().jssa_pages_fork(
+        C.byref(L), s, _packed(dst, torch.int32, (n,), "dst", dev), n,
+        *_book(L, page_table, ref_count, seq_lens, dev), *_ws(ws, dev), _stream(stream, dev))
+    _check("jssa_pages_fork", code)
 
 
 def pages_reserve(L, n_new, page_table, ref_count, seq_lens, copy_src, copy_dst, ws, stream=None):
     """Room for n_new[b] more tokens of every sequence, added to seq_lens; copy_src/copy_dst [B]
     name the shared pages to copy (pages_copy) before the append."""
-    w, n = _ws(ws)
-    _check("jssa_pages_reserve", load().jssa_pages_reserve(
-        C.byref(L), _i32(n_new, (L.B,), "n_new"), *_book(L, page_table, ref_count, seq_lens),
-        _i32(copy_src, (L.B,), "copy_src"), _i32(copy_dst, (L.B,), "copy_dst"), w, n, _stream(stream)))
+    dev, B = _device(), (L.B,)
+    code = load().jssa_pages_reserve(
+        C.byref(L), _packed(n_new, torch.int32, B, "n_new", dev), *_book(L, page_table, ref_count, seq_lens, dev),
+        _packed(copy_src, torch.int32, B, "copy_src", dev), _packed(copy_dst, torch.int32, B, "copy_dst", dev),
+        *_ws(ws, dev), _stream(stream, dev))
+    _check("jssa_pages_reserve", code)
 
 
 def pages_release(L, ended, window: int, n_sinks: int, page_table, ref_count, seq_lens, ws, stream=None):
     """Give up all pages of the sequences with ended[b] != 0 and, with window > 0, the others' pages
     behind their last `window` tokens that hold none of the first n_sinks."""
-    e = _i32(ended, (L.B,), "ended") if ended is not None else None
-    w, n = _ws(ws)
-    _check("jssa_pages_release", load().jssa_pages_release(
-        C.byref(L), e, window, n_sinks, *_book(L, page_table, ref_count, seq_lens), w, n, _stream(stream)))
+    dev = _device()
+    code = load().jssa_pages_release(
+        C.byref(L), None if ended is None else _packed(ended, torch.int32, (L.B,), "ended", dev), window, n_sinks,
+        *_book(L, page_table, ref_count, seq_lens, dev), *_ws(ws, dev), _stream(stream, dev))
+    _check("jssa_pages_release", code)
 
 
 def pages_compact(L, page_table, ref_count, src, dst, n_moves, ws, stream=None):
     """Move the pages in use to the front of the pool (at most len(src) of them): the table and the
     counts now, the rows with pages_copy(..., src, dst, n_moves)."""
-    s = _i32(src, (-1,), "src")
-    w, n = _ws(ws)
-    _check("jssa_pages_compact", load().jssa_pages_compact(
-        C.byref(L), _i32(page_table, (L.B, L.max_pages), "page_table"), _i32(ref_count, (L.n_pages,), "ref_count"),
-        s, _i32(dst, (src.shape[0],), "dst"), src.shape[0], _i32(n_moves, (1,), "n_moves"), w, n, _stream(stream)))
+    dev = _device()
+    s, n = _list(src, "src", dev)
+    code = load().jssa_pages_compact(
+        C.byref(L), _table(L, page_table, dev), _packed(ref_count, torch.int32, (L.n_pages,), "ref_count", dev), s,
+        _packed(dst, torch.int32, (n,), "dst", dev), n, _packed(n_moves, torch.int32, (1,), "n_moves", dev),
+        *_ws(ws, dev), _stream(stream, dev))
+    _check("jssa_pages_compact", code)
 
 
 def pages_copy(L, K, V, src, dst, count=None, ws=None, stream=None):
     """Copy page src[i] over page dst[i] in both pools, for every entry or the first count[0];
     negative entries are skipped."""
-    s = _i32(src, (-1,), "src")
-    c = _i32(count, (1,), "count") if count is not None else None
-    w, n = _ws(ws)
-    _check("jssa_pages_copy", load().jssa_pages_copy(
-        C.byref(L), _pool(L, K, L.k_stride, "K"), _pool(L, V, L.v_stride, "V"), s,
-        _i32(dst, (src.shape[0],), "dst"), src.shape[0], c, w, n, _stream(stream)))
+    dev = _device()
+    s, n = _list(src, "src", dev)
+    code = load().jssa_pages_copy(
+        C.byref(L), *_pools(L, K, V, dev), s, _packed(dst, torch.int32, (n,), "dst", dev), n,
+        None if count is None else _packed(count, torch.int32, (1,), "count", dev), *_ws(ws, dev),
+        _stream(stream, dev))
+    _check("jssa_pages_copy", code)
