@@ -32,6 +32,8 @@
 // the item sees: P is 0 there, but such rows may hold infinities or NaN.
 // Every wait is bounded; on a timeout the kernel raises DEVFLAG_TIMEOUT, all roles leave their
 // loops, copies and MMAs in flight are drained, and tensor memory is freed.
+#include <type_traits>
+
 #include <cuda.h>
 
 #include "common.cuh"
@@ -45,6 +47,8 @@ namespace {
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kPaOCol = 256;   // first TMEM column of O; S (and P over it) below
 constexpr float kPaRescale = 8.f;   // log2 margin before the running maximum moves
+constexpr int kPaCubicEvery = 4;    // of so many pairs of exponentials, one goes to the FMA pipe
+constexpr int kPaPieces = 4;        // pieces published at once
 constexpr int kPaBadRing = 16;      // tiles whose missing pages are remembered
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -60,7 +64,7 @@ struct Pa {
   // with the static arrays (3 KB, a multiple of the dynamic array's alignment) all of an SM's shared memory for d = 128
   static constexpr int kSmem = kWG * kQBytes + kStages * kStageBytes;
   static constexpr int kSoftmax = kWG * 128;             // softmax threads
-  static constexpr int kThreads = kSoftmax + 96;
+  static constexpr int kThreads = kSoftmax + (kWG == 2 ? 128 : 96);
   static constexpr int kPer = (1024 + kThreads - 1) / kThreads;  // sequences per thread in the prologue
   static constexpr uint32_t kSCols = kTile;              // columns of one S slot (two slots)
 };
@@ -106,9 +110,11 @@ __device__ __forceinline__ Item item_at(const PaParams& p, int nq, int len, int 
   return it;
 }
 
-// An item's length on the line: a tile of two query tiles counts twice.
+// An item's length on the line: a tile of two query tiles counts twice, and what a piece costs
+// before its first tile and after its last stands at the front.
+constexpr int kPaItemUnits = 2;
 __device__ __forceinline__ int64_t item_units(const Item& it) {
-  return it.solo ? it.ntiles : 2 * static_cast<int64_t>(it.ntiles);
+  return kPaItemUnits + (it.solo ? it.ntiles : 2 * static_cast<int64_t>(it.ntiles));
 }
 
 // The CTAs' cuts of the line and this CTA's first item, written once by the prologue.
@@ -117,60 +123,67 @@ struct Line {
   int nact, b, h, j;
 };
 
-// Walks the pieces of items that fall to this CTA, in order.
-template <int D>
-struct Pieces {
-  const PaParams& p;
-  int64_t u, u0, u1, total, q0_b;
-  int nact, nb, nh, nj, nq_b, len_b;
-  // the current piece
+// A CTA's share of one item: tiles [t0, t1); t1 = 0 ends the CTA's work.  CTAs c_first to c_last share the item.
+struct Piece {
   Item it;
+  int64_t q0;  // first token's row
   int b, h, t0, t1, c_first, c_last;
-  int64_t q0;
+};
 
-  __device__ Pieces(const PaParams& pp, const Line& s) : p(pp) {
+// Walks the pieces that fall to this CTA, in order.
+template <int D>
+struct Walk {
+  const PaParams& p;
+  int64_t u, u0, u1, total, q0;
+  int nact, b, h, j, nq, len;
+
+  __device__ Walk(const PaParams& pp, const Line& s) : p(pp) {
     total = s.total;
     nact = s.nact;
     u0 = blockIdx.x * total / nact;
     u1 = (blockIdx.x + 1) * total / nact;
     u = s.start;
-    nb = s.b, nh = s.h, nj = s.j;
+    b = s.b, h = s.h, j = s.j;
     load();
   }
   __device__ void load() {
-    const NewTokens t = new_tokens(p.a.q_begin, p.a.seq_lens, nb,
+    const NewTokens t = new_tokens(p.a.q_begin, p.a.seq_lens, b,
                                    static_cast<int64_t>(p.a.max_pages) * p.a.pool.page_size, p.a.n_tokens,
                                    p.a.max_q_len, nullptr);
-    q0_b = t.q0, nq_b = t.nq, len_b = t.len;
+    q0 = t.q0, nq = t.nq, len = t.len;
   }
   __device__ int owner(int64_t x) const { return static_cast<int>(((x + 1) * nact + total - 1) / total) - 1; }
-  __device__ bool next() {
+  __device__ Piece next() {
+    Piece c;
+    c.t1 = 0;
     while (u < u1) {
-      it = item_at<D>(p, nq_b, len_b, nj);
-      const int w = it.solo ? 1 : 2;
-      t0 = u >= u0 ? 0 : static_cast<int>((u0 - u + w - 1) / w);
-      t1 = static_cast<int>(min64(it.ntiles, (u1 - u + w - 1) / w));
-      b = nb, h = nh, q0 = q0_b + it.tok0;
-      const bool mine = t0 < t1;
-      if (mine) {
-        c_first = owner(u);
-        c_last = owner(u + static_cast<int64_t>(w) * (it.ntiles - 1));
-      }
-      u += item_units(it);
-      ++nj;
-      if (it.tok0 + it.ntok == nq_b) {
-        nj = 0;
-        if (++nh == p.a.pool.Hkv) {
-          nh = 0;
+      c.it = item_at<D>(p, nq, len, j);
+      const int w = c.it.solo ? 1 : 2;
+      const int64_t at = u + kPaItemUnits;  // tile i belongs to the CTA that has place at + w i
+      c.t0 = at >= u0 ? 0 : static_cast<int>((u0 - at + w - 1) / w);
+      c.t1 = at >= u1 ? 0 : static_cast<int>(min64(c.it.ntiles, (u1 - at + w - 1) / w));
+      c.b = b, c.h = h, c.q0 = q0 + c.it.tok0;
+      u += item_units(c.it);
+      ++j;
+      if (c.it.tok0 + c.it.ntok == nq) {
+        j = 0;
+        if (++h == p.a.pool.Hkv) {
+          h = 0;
           do {
-            if (++nb == p.a.B) break;
+            if (++b == p.a.B) break;
             load();
-          } while (nq_b == 0);
+          } while (nq == 0);
         }
       }
-      if (mine) return true;
+      if (c.t0 < c.t1) {
+        c.c_first = c.t0 == 0 ? static_cast<int>(blockIdx.x) : owner(at);
+        c.c_last = c.t1 == c.it.ntiles ? static_cast<int>(blockIdx.x)
+                                       : owner(at + static_cast<int64_t>(w) * (c.it.ntiles - 1));
+        return c;
+      }
+      c.t1 = 0;
     }
-    return false;
+    return c;
   }
 };
 
@@ -200,10 +213,54 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
+__device__ __forceinline__ void prefetch_tensormap(const void* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// Two fp32 values in one 64-bit register, and the packed arithmetic on them.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// 2^x of two values on the FMA pipe, for -126 <= x < 127 (lower ones count as -126): x = n + f with
+// n the nearest integer, read off the low bits of x + 1.5 2^23, and 2^f on [-1/2, 1/2] by the
+// cubic of least maximal relative error (7.5e-5, found by exchange; p is rounded to bf16, 3.9e-3).
+__device__ __forceinline__ uint64_t exp2_cubic2(uint64_t x) {
+  float a, b, na, nb;
+  unpack2(x, a, b);
+  x = pack2(fmaxf(a, -126.f), fmaxf(b, -126.f));
+  const uint64_t magic = pack2(12582912.f, 12582912.f);
+  const uint64_t t = add2(x, magic);
+  const uint64_t n = add2(t, pack2(-12582912.f, -12582912.f));
+  const uint64_t f = fma2(n, pack2(-1.f, -1.f), x);
+  uint64_t y = fma2(f, pack2(0.0551716685f, 0.0551716685f), pack2(0.242611125f, 0.242611125f));
+  y = fma2(y, f, pack2(0.693260968f, 0.693260968f));
+  y = fma2(y, f, pack2(0.999928057f, 0.999928057f));
+  unpack2(y, a, b);
+  unpack2(t, na, nb);
+  return pack2(__uint_as_float(__float_as_uint(a) + (__float_as_uint(na) << 23)),
+               __uint_as_float(__float_as_uint(b) + (__float_as_uint(nb) << 23)));
 }
 
 // Bits [0, n) of a word, n clamped to [0, 32].
@@ -211,7 +268,7 @@ __device__ __forceinline__ uint32_t bits_below(int n) { return n <= 0 ? 0u : (n 
 
 // Page of this lane's box of tile i: -2 where the item has no keys, -1 where the table names no page.
 template <int D>
-__device__ __forceinline__ int box_page(const PaParams& p, const Pieces<D>& s, int i, int box, bool on, int* t_out) {
+__device__ __forceinline__ int box_page(const PaParams& p, const Piece& s, int i, int box, bool on, int* t_out) {
   const int v = i * Pa<D>::kTile + box * p.box;
   if (!on || v >= s.it.nv) return -2;
   const int t = v < s.it.s_al ? v : v + s.it.shift;
@@ -249,7 +306,8 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
   constexpr int kTile = C::kTile, kWG = C::kWG, kDB = C::kDB, kNS = C::kStages;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t q_full, q_empty, kv_full[kNS], kv_empty[kNS], edge_full[kNS], s_full[2], p_full[2],
-      o_full[2], wg_bar, drain;
+      o_full[2], piece_full[kPaPieces], piece_empty[kPaPieces], wg_bar, drain;
+  __shared__ Piece pieces[kPaPieces];
   __shared__ Line line;
   __shared__ int64_t warp_sum[C::kThreads / 32];
   __shared__ uint32_t tmem_base_s, bad_s[kPaBadRing];
@@ -259,6 +317,12 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const PagedAttnArgs& a = p.a;
   const int64_t cap = static_cast<int64_t>(a.max_pages) * a.pool.page_size;
+
+  if (tid == 0) {
+    prefetch_tensormap(&p.q);
+    prefetch_tensormap(&p.k);
+    prefetch_tensormap(&p.v);
+  }
 
   // ---- the line: every CTA adds up all sequences' items (a few consecutive ones per thread)
   int64_t mine = 0, units[C::kPer];
@@ -325,6 +389,10 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
       mbar_init(&p_full[i], 128);
       mbar_init(&o_full[i], 1);
     }
+    for (int i = 0; i < kPaPieces; ++i) {
+      mbar_init(&piece_full[i], 1);
+      mbar_init(&piece_empty[i], C::kSoftmax / 32 + 2);
+    }
     mbar_init(&wg_bar, C::kSoftmax);
     mbar_init(&drain, 1);
     fence_mbarrier_init();
@@ -369,199 +437,39 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
   const uint32_t base = smem_u32(smem_raw);
   const uint32_t q_s = base, kv_s = base + kWG * C::kQBytes;
   const Waiter wait{&dead_s, a.status};
-  Pieces<D> s(p, line);
-
-  if (warp == kLoadWarp) {
-    // ------------------------------------------------------------------ loads
-    const int box = lane / kDB, db = lane % kDB;
-    const bool on = box < p.nbox;
-    uint32_t n = 0, tiles = 0;  // ring places filled; tiles begun
-    bool ok = true;
-    for (int piece = 0; ok && s.next(); ++piece) {
-      if (piece > 0) ok = __all_sync(0xFFFFFFFFu, wait(&q_empty, (piece - 1) & 1));
-      if (!ok) break;
-      const int nqt = s.it.solo ? 1 : 2;
-      if (lane == 0) mbar_arrive_expect_tx(&q_full, nqt * kDB * p.tpt * p.G * 128);
-      __syncwarp();
-      if (lane < nqt * kDB)
-        tma_load_3d(q_s + (lane / kDB) * C::kQBytes + db * C::kQBlock, &p.q, db * 64, s.h * p.G,
-                    static_cast<int>(s.q0) + (lane / kDB) * p.tpt, &q_full);
-      int t_next = 0, t_prev = 0, pg_prev = -2;
-      int pg_next = box_page<D>(p, s, s.t0, box, on, &t_next);
-      // step i: K of tile i, V of tile i - 1
-      for (int i = s.t0; ok && i <= s.t1; ++i) {
-        const int pg = pg_next, t = t_next;
-        pg_next = -2;
-        if (i + 1 < s.t1) pg_next = box_page<D>(p, s, i + 1, box, on, &t_next);
-        for (int kv = 0; kv < 2; ++kv) {
-          const bool is_v = kv == 1;
-          if (is_v ? i == s.t0 : i == s.t1) continue;
-          const int pgx = is_v ? pg_prev : pg, tx = is_v ? t_prev : t;
-          const uint32_t st = n % kNS;
-          if (n >= kNS) ok = __all_sync(0xFFFFFFFFu, wait(&kv_empty[st], ((n / kNS) & 1) ^ 1));
-          if (!ok) break;
-          const uint32_t bad = __ballot_sync(0xFFFFFFFFu, pgx == -1);
-          const uint32_t loads = __popc(__ballot_sync(0xFFFFFFFFu, pgx >= 0));
-          uint64_t* bar = &kv_full[st];
-          if (is_v && (bad || edge_tile<D>(s.it, i - 1))) bar = &edge_full[st];
-          if (lane == 0) {
-            if (!is_v) {
-              bad_s[tiles % kPaBadRing] = bad;
-              if (bad) flag_error(a.status, DEVFLAG_BAD_INDEX);
-            }
-            mbar_arrive_expect_tx(bar, loads * p.box * 128);
-          }
-          if (!is_v) ++tiles;
-          __syncwarp();
-          if (pgx >= 0)
-            tma_load_4d(kv_s + st * C::kStageBytes + db * (kTile * 128) + box * p.box * 128, is_v ? &p.v : &p.k,
-                        db * 64, tx % a.pool.page_size, s.h, pgx, bar);
-          ++n;
-        }
-        pg_prev = pg;
-        t_prev = t;
-      }
-    }
-    if (!ok) {  // wait for the copies in flight
-      if (lane == 0)
-        for (uint32_t i = n > kNS ? n - kNS : 0; i < n; ++i)
-          mbar_wait_bounded(&kv_full[i % kNS], (i / kNS) & 1, a.status);
-    }
-  } else if (warp == kZeroWarp) {
-    // ------------------------------------------------------------------ unseen V rows
-    const int box = lane / kDB;
-    const bool on = box < p.nbox;
-    uint32_t n0 = 0, par = 0;  // ring place of the piece; phase of each edge barrier
-    bool ok = true;
-    while (ok && s.next()) {
-      const int nt = s.t1 - s.t0;
-      for (int i = s.t0; ok && i < s.t1; ++i) {
-        int t = 0;
-        const uint32_t bad = __ballot_sync(0xFFFFFFFFu, box_page<D>(p, s, i, box, on, &t) == -1);
-        if (!bad && !edge_tile<D>(s.it, i)) continue;
-        const uint32_t st = (n0 + v_place(i - s.t0, nt)) % kNS;
-        ok = __all_sync(0xFFFFFFFFu, wait(&edge_full[st], (par >> st) & 1));
-        if (!ok) break;
-        par ^= 1u << st;
-        for (int r = lane; r < kTile; r += 32) {
-          const int v = i * kTile + r;
-          const bool lost = (bad >> ((r / p.box) * kDB)) & 1;
-          if (lost || v >= s.it.nv || (v >= s.it.z0 && v < s.it.z1)) {
-#pragma unroll
-            for (int x = 0; x < kDB * 8; ++x)
-              st_shared_v4(kv_s + st * C::kStageBytes + (x >> 3) * (kTile * 128) + r * 128 + (x & 7) * 16, 0, 0, 0, 0);
-          }
-        }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&kv_full[st]);
-      }
-      n0 += 2 * nt;
-    }
-  } else if (warp == kMmaWarp) {
-    // ------------------------------------------------------------------ MMAs
-    if (lane == 0) {
-      const uint32_t idesc_s = instr_desc(128, kTile, false, false);
-      const uint32_t idesc_o = instr_desc(128, D, true, false);
-      uint32_t n0 = 0, np[2] = {0, 0};
-      bool ok = true;
-      auto full = [&](uint32_t place) { return wait(&kv_full[place % kNS], (place / kNS) & 1); };
-      auto scores = [&](int slot, int qt, uint32_t place) {
-        const uint32_t qa = q_s + qt * C::kQBytes, ka = kv_s + (place % kNS) * C::kStageBytes;
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          umma_bf16(tmem + slot * C::kSCols, smem_desc(qa + (kk >> 2) * C::kQBlock + (kk & 3) * 32, 16, 1024),
-                    smem_desc(ka + (kk >> 2) * (kTile * 128) + (kk & 3) * 32, 16, 1024), idesc_s, kk != 0);
-      };
-      auto values = [&](int slot, int o, uint32_t place, bool first) {
-        const uint32_t va = kv_s + (place % kNS) * C::kStageBytes;
-#pragma unroll
-        for (int part = 0; part < (F32 ? 2 : 1); ++part)
-#pragma unroll
-          for (int kt = 0; kt < kTile / 16; ++kt)
-            umma_bf16_ts(tmem + kPaOCol + o * D, tmem + slot * C::kSCols + part * (kTile / 2) + kt * 8,
-                         smem_desc(va + kt * 2048, kTile * 128, 1024), idesc_o, !first || part || kt);
-      };
-      for (int piece = 0; ok && s.next(); ++piece) {
-        const int n = s.t1 - s.t0;
-        const bool pair = !s.it.solo;
-        ok = wait(&q_full, piece & 1) && full(n0);
-        if (!ok) break;
-        tc_fence_after();
-        for (int st = 0; st < (pair ? 2 : 1); ++st) {
-          scores(st, st, n0);
-          umma_commit(&s_full[st]);
-        }
-        umma_commit(&kv_empty[n0 % kNS]);
-        if (n == 1) umma_commit(&q_empty);
-        if (!pair && n > 1) {
-          ok = full(n0 + k_place(1));
-          if (!ok) break;
-          scores(1, 0, n0 + k_place(1));
-          umma_commit(&s_full[1]);
-          umma_commit(&kv_empty[(n0 + k_place(1)) % kNS]);
-          if (n == 2) umma_commit(&q_empty);
-        }
-        for (int i = 0; ok && i < n; ++i) {
-          const uint32_t vp = n0 + v_place(i, n);
-          if (pair) {
-            const uint32_t kp = n0 + k_place(i + 1);
-            ok = (i + 1 == n || full(kp)) && full(vp);
-            for (int st = 0; ok && st < 2; ++st) {
-              ok = wait(&p_full[st], np[st]++ & 1);
-              if (!ok) break;
-              tc_fence_after();
-              values(st, st, vp, i == 0);
-              if (st == 1) umma_commit(&kv_empty[vp % kNS]);
-              umma_commit(&o_full[st]);
-              if (i + 1 < n) {
-                scores(st, st, kp);
-                if (st == 1) {
-                  umma_commit(&kv_empty[kp % kNS]);
-                  if (i + 2 == n) umma_commit(&q_empty);
-                }
-                umma_commit(&s_full[st]);
-              }
-            }
-          } else {
-            const int slot = i & 1, o = kWG == 2 ? slot : 0;
-            ok = full(vp) && wait(&p_full[slot], np[slot]++ & 1);
-            if (!ok) break;
-            tc_fence_after();
-            values(slot, o, vp, i == 0 || (kWG == 2 && i == 1));
-            umma_commit(&kv_empty[vp % kNS]);
-            umma_commit(&o_full[slot]);
-            if (i + 2 < n) {
-              const uint32_t kp = n0 + k_place(i + 2);
-              ok = full(kp);
-              if (!ok) break;
-              scores(slot, 0, kp);
-              umma_commit(&kv_empty[kp % kNS]);
-              if (i + 3 == n) umma_commit(&q_empty);
-              umma_commit(&s_full[slot]);
-            }
-          }
-        }
-        n0 += 2 * n;
-      }
-      umma_commit(&drain);  // every MMA and commit before it, in the error case too
-      mbar_wait_bounded(&drain, 0, a.status);
-    }
+  // The load warp walks the pieces and publishes them; every other warp takes them in order.
+  auto take = [&](int k, bool* ok) -> const Piece& {
+    *ok = __all_sync(0xFFFFFFFFu, wait(&piece_full[k % kPaPieces], (k / kPaPieces) & 1)) != 0;
+    if (*ok && pieces[k % kPaPieces].t1 == 0) *ok = false;
+    return pieces[k % kPaPieces];
+  };
+  auto release = [&](int k) {
     __syncwarp();
-  } else {
+    if (lane == 0) mbar_arrive(&piece_empty[k % kPaPieces]);
+  };
+
+  // Two softmax warpgroups at 208 registers and the other four warps at 88 make up the launch's 384 x 168
+  // (the split stands at the head of each branch, where the compiler can use it).
+  if (warp < kMmaWarp) {
     // ------------------------------------------------------------------ softmax and output
+    if constexpr (kWG == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int wg = warp >> 2, quad = warp & 3;
     const int r = quad * 32 + lane, tr = r / p.G;
     const int rows_tile = p.tpt * p.G;
     const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    uint32_t ns[2] = {0, 0}, no[2] = {0, 0}, tiles0 = 0, nwg = 0;  // barrier phases; tiles before the piece
+    uint32_t s_par = 0, o_par = 0;    // phases of s_full and o_full, a bit per slot
+    uint32_t tiles0 = 0, wg_par = 0;  // tiles before the piece
     bool ok = true;
     auto all_ok = [&](bool x) { return __all_sync(0xFFFFFFFFu, x) != 0; };
     auto sync_wgs = [&]() {
       mbar_arrive(&wg_bar);
-      return all_ok(wait(&wg_bar, nwg++ & 1));
+      const bool x = all_ok(wait(&wg_bar, wg_par));
+      wg_par ^= 1;
+      return x;
     };
-    while (ok && s.next()) {
+    for (int piece = 0; ok; ++piece) {
+      const Piece& s = take(piece, &ok);
+      if (!ok) break;
       const bool solo = s.it.solo;
       const int qoff = !solo && wg == 1 ? p.tpt : 0;
       const bool valid = r < rows_tile && qoff + tr < s.it.ntok;
@@ -576,19 +484,22 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
       const int o_slot = kWG == 2 ? wg : 0;
       float m = -INFINITY, l = 0.f;
       bool first = true;
-      int prev = 0;  // slot of the tile before: a barrier per slot, since with one warpgroup two products may be under way
+      int prev = 0;  // slot of the tile before (with one warpgroup two products may be under way, hence a barrier each)
       for (int i = s.t0 + (split_keys ? wg : 0); i < s.t1; i += split_keys ? 2 : 1) {
         const int slot = kWG == 2 ? wg : ((i - s.t0) & 1);
-        ok = all_ok(wait(&s_full[slot], ns[slot]++ & 1));
+        ok = all_ok(wait(&s_full[slot], (s_par >> slot) & 1));
+        s_par ^= 1u << slot;
         if (!ok) break;
         tc_fence_after();
         if (active) {
-          float x[kTile];
-          if constexpr (kTile == 128) tmem_ld128(trow + slot * C::kSCols, x);
-          else tmem_ld64(trow + slot * C::kSCols, x);
+          const uint32_t s_col = trow + slot * C::kSCols;
           const int v0 = i * kTile;
           const uint32_t bad = bad_s[(tiles0 + i - s.t0) % kPaBadRing];
-          if (bad || v0 < b_max || v0 + kTile > c_min) {
+          const bool masked = bad || v0 < b_max || v0 + kTile > c_min;
+          float x[kTile];
+          if constexpr (kTile == 128) tmem_ld128(s_col, x);
+          else tmem_ld64(s_col, x);
+          if (masked) {
 #pragma unroll
             for (int c = 0; c < kTile / 32; ++c) {
               const int at = v0 + 32 * c;
@@ -601,15 +512,14 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
               for (int e = 0; e < 32; ++e) x[32 * c + e] = (w >> e) & 1 ? x[32 * c + e] : -INFINITY;
             }
           }
-          float mx0 = x[0], mx1 = x[1], mx2 = x[2], mx3 = x[3];
+          float m4[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-          for (int e = 4; e < kTile; e += 4) {
-            mx0 = fmaxf(mx0, x[e]);
-            mx1 = fmaxf(mx1, x[e + 1]);
-            mx2 = fmaxf(mx2, x[e + 2]);
-            mx3 = fmaxf(mx3, x[e + 3]);
+          for (int e = 4; e < kTile; e += 8) {
+#pragma unroll
+            for (int f = 0; f < 4; ++f)
+              m4[f] = fmaxf(fmaxf(m4[f], x[e + f]), e + 4 + f < kTile ? x[e + 4 + f] : -INFINITY);
           }
-          const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
+          const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
           const bool move = m == -INFINITY ? mx > -INFINITY : (mx - m) * p.scale_log2 > kPaRescale;
           if (__any_sync(0xFFFFFFFFu, move)) {
             float alpha = 1.f;
@@ -619,7 +529,7 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
               l *= alpha;
             }
             if (!first) {  // the products before this tile have to be done
-              ok = all_ok(wait(&o_full[prev], (no[prev] - 1) & 1));
+              ok = all_ok(wait(&o_full[prev], ((o_par >> prev) & 1) ^ 1));
               if (!ok) break;
               tc_fence_after();
 #pragma unroll 1
@@ -633,28 +543,47 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
             }
           }
           const float mm = m == -INFINITY ? 0.f : m * p.scale_log2;
-          float l0 = 0.f, l1 = 0.f;
+          const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2), mm2 = pack2(-mm, -mm);
+          uint64_t l2[2] = {0, 0};
+          // P over the scores it comes from: in the first 16 of 32 columns, its remainder in the other 16
+          auto exponentials = [&](auto cubic) {
 #pragma unroll
-          for (int c = 0; c < kTile / 32; ++c) {
-            uint32_t hi[16], lo[16];
+            for (int c = 0; c < kTile / 32; ++c) {
+              uint32_t hi[16], lo[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float p0 = exp2_approx(fmaf(x[32 * c + 2 * e], p.scale_log2, -mm));
-              const float p1 = exp2_approx(fmaf(x[32 * c + 2 * e + 1], p.scale_log2, -mm));
-              l0 += p0;
-              l1 += p1;
-              hi[e] = pack_bf16x2(p0, p1);
-              if constexpr (F32)
-                lo[e] = pack_bf16x2(p0 - bf16_bits_to_float(hi[e] & 0xFFFFu), p1 - __uint_as_float(hi[e] & 0xFFFF0000u));
+              for (int e = 0; e < 16; ++e) {
+                const uint64_t z = fma2(pack2(x[32 * c + 2 * e], x[32 * c + 2 * e + 1]), scale2, mm2);
+                float p0, p1;
+                uint64_t pp;
+                if (cubic && e % kPaCubicEvery == kPaCubicEvery - 1) {
+                  pp = exp2_cubic2(z);
+                  unpack2(pp, p0, p1);
+                } else {
+                  unpack2(z, p0, p1);
+                  p0 = exp2_approx(p0);
+                  p1 = exp2_approx(p1);
+                  pp = pack2(p0, p1);
+                }
+                l2[e & 1] = add2(l2[e & 1], pp);
+                hi[e] = pack_bf16x2(p0, p1);
+                if constexpr (F32)
+                  lo[e] =
+                      pack_bf16x2(p0 - bf16_bits_to_float(hi[e] & 0xFFFFu), p1 - __uint_as_float(hi[e] & 0xFFFF0000u));
+              }
+              tmem_st16_nowait(s_col + 32 * c, hi);
+              if constexpr (F32) tmem_st16_nowait(s_col + 32 * c + 16, lo);
             }
-            tmem_st16_nowait(trow + slot * C::kSCols + 16 * c, hi);
-            if constexpr (F32) tmem_st16_nowait(trow + slot * C::kSCols + kTile / 2 + 16 * c, lo);
-          }
-          l += l0 + l1;
+          };
+          // the cubic takes -infinity for 2^-126, which masked scores must not be
+          if (F32 || kWG == 1 || masked) exponentials(std::false_type());
+          else exponentials(std::true_type());
+          float la, lb;
+          unpack2(add2(l2[0], l2[1]), la, lb);
+          l += la + lb;
           tmem_st_wait();
         }
         first = false;
-        ++no[slot];
+        o_par ^= 1u << slot;
         prev = slot;
         tc_fence_before();
         mbar_arrive(&p_full[slot]);
@@ -662,7 +591,7 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
       tiles0 += s.t1 - s.t0;
       if (!ok) break;
       if (!first) {
-        ok = all_ok(wait(&o_full[prev], (no[prev] - 1) & 1));
+        ok = all_ok(wait(&o_full[prev], ((o_par >> prev) & 1) ^ 1));
         if (!ok) break;
       }
       // the row's factor on each accumulator that holds a share of it
@@ -715,6 +644,7 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
       tc_fence_before();
       if (whole) {
         if (split_keys) ok = sync_wgs();  // neither accumulator is overwritten before both have read it
+        release(piece);
         continue;
       }
       // ---- the last CTA of a cut item merges its pieces
@@ -734,34 +664,301 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
         __threadfence();
         const int n = s.c_last - s.c_first + 1;
         const int rows = s.it.ntok * p.G;
-        for (int idx = tid; idx < rows * (D / 4); idx += C::kSoftmax) {
-          const int rr = idx / (D / 4), c = idx % (D / 4);
-          auto at = [&](int k) {
-            return static_cast<int64_t>(2 * (s.c_first + k) + (k == 0 ? 1 : 0)) * a.rows_cap + rr;
-          };
+        // partial k of a row; the first piece of an item is the last of its CTA, the others the first of theirs
+        auto at = [&](int k, int row) {
+          return static_cast<int64_t>(2 * (s.c_first + k) + (k == 0 ? 1 : 0)) * a.rows_cap + row;
+        };
+        // each row's maximum and 1 / sum: a thread per row, or a warp where there are few
+        float* row_m = &ml_s[0][0][0];
+        float* row_g = row_m + C::kSoftmax;
+        const bool by_warp = rows <= 4 * (C::kSoftmax / 32);
+        for (int rr = by_warp ? warp : tid; rr < rows; rr += by_warp ? C::kSoftmax / 32 : C::kSoftmax) {
           float M = -INFINITY, L = 0.f;
-          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+          const int k0 = by_warp ? lane : 0, kstep = by_warp ? 32 : 1;
 #pragma unroll 4
-          for (int k = 0; k < n; ++k) M = fmaxf(M, __ldcg(&a.part_ml[at(k)].x));
-#pragma unroll 4
-          for (int k = 0; k < n; ++k) {
-            const float2 ml = __ldcg(&a.part_ml[at(k)]);
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + at(k) * D) + c);
-            const float w = ml.y > 0.f ? exp2_approx((ml.x - M) * p.scale_log2) : 0.f;
-            L = fmaf(w, ml.y, L);
-            o.x = fmaf(w, v.x, o.x), o.y = fmaf(w, v.y, o.y), o.z = fmaf(w, v.z, o.z), o.w = fmaf(w, v.w, o.w);
+          for (int k = k0; k < n; k += kstep) {
+            const float2 ml = __ldcg(&a.part_ml[at(k, rr)]);
+            const float mn = fmaxf(M, ml.x);
+            if (ml.y > 0.f) {
+              L = L * exp2_approx((M - mn) * p.scale_log2) + ml.y * exp2_approx((ml.x - mn) * p.scale_log2);
+              M = mn;
+            }
           }
-          const float g = L > 0.f ? 1.f / L : 0.f;
-          o.x *= g, o.y *= g, o.z *= g, o.w *= g;
-          const int64_t to = (s.q0 + rr / p.G) * a.Hq + s.h * p.G + rr % p.G;
-          if constexpr (F32)
-            reinterpret_cast<float4*>(static_cast<float*>(a.O) + to * D)[c] = o;
-          else
-            reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.O) + to * D)[c] =
-                make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
-          if (c == 0 && a.lse) a.lse[to] = L > 0.f ? M * a.sm_scale + logf(L) : -INFINITY;
+          if (by_warp) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+              const float m2 = __shfl_xor_sync(0xFFFFFFFFu, M, o), l2 = __shfl_xor_sync(0xFFFFFFFFu, L, o);
+              const float mn = fmaxf(M, m2);
+              L = (L > 0.f ? L * exp2_approx((M - mn) * p.scale_log2) : 0.f) +
+                  (l2 > 0.f ? l2 * exp2_approx((m2 - mn) * p.scale_log2) : 0.f);
+              M = mn;
+            }
+          }
+          if (!by_warp || lane == 0) {
+            row_m[rr] = M;
+            row_g[rr] = L > 0.f ? 1.f / L : 0.f;
+            if (a.lse)
+              a.lse[(s.q0 + rr / p.G) * a.Hq + s.h * p.G + rr % p.G] = L > 0.f ? M * a.sm_scale + logf(L) : -INFINITY;
+          }
+        }
+        ok = sync_wgs();
+        if (!ok) break;
+        // sums over the partials; with fewer 16-byte words than threads, 2^sh lanes share a word
+        const int words = rows * (D / 4);
+        int sh = 0;
+        while (sh < 5 && (words << (sh + 1)) <= C::kSoftmax) ++sh;
+        const int part = tid & ((1 << sh) - 1), wstep = C::kSoftmax >> sh;
+        constexpr int kBatch = 4;  // words of a thread under way at once
+        for (int w0 = 0; w0 < words; w0 += kBatch * wstep) {
+          float4 o[kBatch];
+          float wm[kBatch], wg2[kBatch];
+          int rr[kBatch], c[kBatch];
+#pragma unroll
+          for (int x = 0; x < kBatch; ++x) {
+            const int idx = w0 + x * wstep + (tid >> sh);
+            rr[x] = idx < words ? idx / (D / 4) : -1;
+            c[x] = idx % (D / 4);
+            wm[x] = row_m[max(rr[x], 0)] * p.scale_log2;
+            wg2[x] = row_g[max(rr[x], 0)];
+            o[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+          for (int k = part; k < n; k += 1 << sh) {
+            float2 ml[kBatch];
+            float4 v[kBatch];
+#pragma unroll
+            for (int x = 0; x < kBatch; ++x) {
+              if (rr[x] < 0) continue;
+              ml[x] = __ldcg(&a.part_ml[at(k, rr[x])]);
+              v[x] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at(k, rr[x]) * D) + c[x]);
+            }
+#pragma unroll
+            for (int x = 0; x < kBatch; ++x) {
+              if (rr[x] < 0) continue;
+              const float w = ml[x].y > 0.f ? wg2[x] * exp2_approx(fmaf(ml[x].x, p.scale_log2, -wm[x])) : 0.f;
+              o[x].x = fmaf(w, v[x].x, o[x].x), o[x].y = fmaf(w, v[x].y, o[x].y);
+              o[x].z = fmaf(w, v[x].z, o[x].z), o[x].w = fmaf(w, v[x].w, o[x].w);
+            }
+          }
+#pragma unroll
+          for (int x = 0; x < kBatch; ++x) {
+            for (int y = 1; y < 1 << sh; y <<= 1) {
+              o[x].x += __shfl_xor_sync(0xFFFFFFFFu, o[x].x, y);
+              o[x].y += __shfl_xor_sync(0xFFFFFFFFu, o[x].y, y);
+              o[x].z += __shfl_xor_sync(0xFFFFFFFFu, o[x].z, y);
+              o[x].w += __shfl_xor_sync(0xFFFFFFFFu, o[x].w, y);
+            }
+            if (part == 0 && rr[x] >= 0) {
+              const int64_t to = (s.q0 + rr[x] / p.G) * a.Hq + s.h * p.G + rr[x] % p.G;
+              if constexpr (F32)
+                reinterpret_cast<float4*>(static_cast<float*>(a.O) + to * D)[c[x]] = o[x];
+              else
+                reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.O) + to * D)[c[x]] =
+                    make_uint2(pack_bf16x2(o[x].x, o[x].y), pack_bf16x2(o[x].z, o[x].w));
+            }
+          }
+        }
+        ok = sync_wgs();  // row_m and row_g are ml_s
+      }
+      release(piece);
+    }
+  } else {
+    if constexpr (kWG == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == kLoadWarp) {
+      // ------------------------------------------------------------------ loads
+      const int box = lane / kDB, db = lane % kDB;
+      const bool on = box < p.nbox;
+      uint32_t n = 0, tiles = 0;  // ring places filled; tiles begun
+      bool ok = true;
+      Walk<D> walk(p, line);
+      for (int piece = 0; ok; ++piece) {
+        const Piece s = walk.next();
+        const int at = piece % kPaPieces;
+        if (piece >= kPaPieces) ok = __all_sync(0xFFFFFFFFu, wait(&piece_empty[at], ((piece / kPaPieces) & 1) ^ 1));
+        if (ok && lane == 0) {
+          pieces[at] = s;
+          mbar_arrive(&piece_full[at]);
+        }
+        if (!ok || s.t1 == 0) break;
+        if (piece > 0) ok = __all_sync(0xFFFFFFFFu, wait(&q_empty, (piece - 1) & 1));
+        if (!ok) break;
+        const int nqt = s.it.solo ? 1 : 2;
+        if (lane == 0) mbar_arrive_expect_tx(&q_full, nqt * kDB * p.tpt * p.G * 128);
+        __syncwarp();
+        if (lane < nqt * kDB)
+          tma_load_3d(q_s + (lane / kDB) * C::kQBytes + db * C::kQBlock, &p.q, db * 64, s.h * p.G,
+                      static_cast<int>(s.q0) + (lane / kDB) * p.tpt, &q_full);
+        int t_next = 0, t_prev = 0, pg_prev = -2;
+        int pg_next = box_page<D>(p, s, s.t0, box, on, &t_next);
+        // step i: K of tile i, V of tile i - 1
+        for (int i = s.t0; ok && i <= s.t1; ++i) {
+          const int pg = pg_next, t = t_next;
+          pg_next = -2;
+          if (i + 1 < s.t1) pg_next = box_page<D>(p, s, i + 1, box, on, &t_next);
+          for (int kv = 0; kv < 2; ++kv) {
+            const bool is_v = kv == 1;
+            if (is_v ? i == s.t0 : i == s.t1) continue;
+            const int pgx = is_v ? pg_prev : pg, tx = is_v ? t_prev : t;
+            const uint32_t st = n % kNS;
+            if (n >= kNS) ok = __all_sync(0xFFFFFFFFu, wait(&kv_empty[st], ((n / kNS) & 1) ^ 1));
+            if (!ok) break;
+            const uint32_t bad = __ballot_sync(0xFFFFFFFFu, pgx == -1);
+            const uint32_t loads = __popc(__ballot_sync(0xFFFFFFFFu, pgx >= 0));
+            uint64_t* bar = &kv_full[st];
+            if (is_v && (bad || edge_tile<D>(s.it, i - 1))) bar = &edge_full[st];
+            if (lane == 0) {
+              if (!is_v) {
+                bad_s[tiles % kPaBadRing] = bad;
+                if (bad) flag_error(a.status, DEVFLAG_BAD_INDEX);
+              }
+              mbar_arrive_expect_tx(bar, loads * p.box * 128);
+            }
+            if (!is_v) ++tiles;
+            __syncwarp();
+            if (pgx >= 0)
+              tma_load_4d(kv_s + st * C::kStageBytes + db * (kTile * 128) + box * p.box * 128, is_v ? &p.v : &p.k,
+                          db * 64, tx % a.pool.page_size, s.h, pgx, bar);
+            ++n;
+          }
+          pg_prev = pg;
+          t_prev = t;
         }
       }
+      if (!ok) {  // wait for the copies in flight
+        if (lane == 0)
+          for (uint32_t i = n > kNS ? n - kNS : 0; i < n; ++i)
+            mbar_wait_bounded(&kv_full[i % kNS], (i / kNS) & 1, a.status);
+      }
+    } else if (warp == kZeroWarp) {
+      // ------------------------------------------------------------------ unseen V rows
+      const int box = lane / kDB;
+      const bool on = box < p.nbox;
+      uint32_t n0 = 0, par = 0;  // ring place of the piece; phase of each edge barrier
+      bool ok = true;
+      for (int piece = 0; ok; ++piece) {
+        const Piece& s = take(piece, &ok);
+        if (!ok) break;
+        const int nt = s.t1 - s.t0;
+        for (int i = s.t0; ok && i < s.t1; ++i) {
+          int t = 0;
+          const uint32_t bad = __ballot_sync(0xFFFFFFFFu, box_page<D>(p, s, i, box, on, &t) == -1);
+          if (!bad && !edge_tile<D>(s.it, i)) continue;
+          const uint32_t st = (n0 + v_place(i - s.t0, nt)) % kNS;
+          ok = __all_sync(0xFFFFFFFFu, wait(&edge_full[st], (par >> st) & 1));
+          if (!ok) break;
+          par ^= 1u << st;
+          for (int r = lane; r < kTile; r += 32) {
+            const int v = i * kTile + r;
+            const bool lost = (bad >> ((r / p.box) * kDB)) & 1;
+            if (lost || v >= s.it.nv || (v >= s.it.z0 && v < s.it.z1)) {
+  #pragma unroll
+              for (int x = 0; x < kDB * 8; ++x)
+                st_shared_v4(kv_s + st * C::kStageBytes + (x >> 3) * (kTile * 128) + r * 128 + (x & 7) * 16, 0, 0, 0,
+                             0);
+            }
+          }
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&kv_full[st]);
+        }
+        n0 += 2 * nt;
+        release(piece);
+      }
+    } else if (warp == kMmaWarp) {
+      // ------------------------------------------------------------------ MMAs
+      if (lane == 0) {
+        const uint32_t idesc_s = instr_desc(128, kTile, false, false);
+        const uint32_t idesc_o = instr_desc(128, D, true, false);
+        uint32_t n0 = 0, p_par = 0;  // ring place of the piece; phases of p_full, a bit per slot
+        bool ok = true;
+        auto full = [&](uint32_t place) { return wait(&kv_full[place % kNS], (place / kNS) & 1); };
+        auto scores = [&](int slot, int qt, uint32_t place) {
+          const uint32_t qa = q_s + qt * C::kQBytes, ka = kv_s + (place % kNS) * C::kStageBytes;
+  #pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            umma_bf16(tmem + slot * C::kSCols, smem_desc(qa + (kk >> 2) * C::kQBlock + (kk & 3) * 32, 16, 1024),
+                      smem_desc(ka + (kk >> 2) * (kTile * 128) + (kk & 3) * 32, 16, 1024), idesc_s, kk != 0);
+        };
+        auto values = [&](int slot, int o, uint32_t place, bool first) {
+          const uint32_t va = kv_s + (place % kNS) * C::kStageBytes;
+  #pragma unroll
+          for (int part = 0; part < (F32 ? 2 : 1); ++part)
+  #pragma unroll
+            for (int kt = 0; kt < kTile / 16; ++kt)
+              umma_bf16_ts(tmem + kPaOCol + o * D, tmem + slot * C::kSCols + (kt >> 1) * 32 + part * 16 + (kt & 1) * 8,
+                           smem_desc(va + kt * 2048, kTile * 128, 1024), idesc_o, !first || part || kt);
+        };
+        for (int piece = 0; ok; ++piece) {
+          const int at = piece % kPaPieces;
+          ok = wait(&piece_full[at], (piece / kPaPieces) & 1);
+          if (!ok || pieces[at].t1 == 0) break;
+          const int n = pieces[at].t1 - pieces[at].t0;
+          const bool pair = !pieces[at].it.solo;
+          mbar_arrive(&piece_empty[at]);
+          ok = wait(&q_full, piece & 1) && full(n0);
+          if (!ok) break;
+          tc_fence_after();
+          for (int st = 0; st < (pair ? 2 : 1); ++st) {
+            scores(st, st, n0);
+            umma_commit(&s_full[st]);
+          }
+          umma_commit(&kv_empty[n0 % kNS]);
+          if (n == 1) umma_commit(&q_empty);
+          if (!pair && n > 1) {
+            ok = full(n0 + k_place(1));
+            if (!ok) break;
+            scores(1, 0, n0 + k_place(1));
+            umma_commit(&s_full[1]);
+            umma_commit(&kv_empty[(n0 + k_place(1)) % kNS]);
+            if (n == 2) umma_commit(&q_empty);
+          }
+          for (int i = 0; ok && i < n; ++i) {
+            const uint32_t vp = n0 + v_place(i, n);
+            if (pair) {
+              const uint32_t kp = n0 + k_place(i + 1);
+              ok = (i + 1 == n || full(kp)) && full(vp);
+              for (int st = 0; ok && st < 2; ++st) {
+                ok = wait(&p_full[st], (p_par >> st) & 1);
+                p_par ^= 1u << st;
+                if (!ok) break;
+                tc_fence_after();
+                values(st, st, vp, i == 0);
+                if (st == 1) umma_commit(&kv_empty[vp % kNS]);
+                umma_commit(&o_full[st]);
+                if (i + 1 < n) {
+                  scores(st, st, kp);
+                  if (st == 1) {
+                    umma_commit(&kv_empty[kp % kNS]);
+                    if (i + 2 == n) umma_commit(&q_empty);
+                  }
+                  umma_commit(&s_full[st]);
+                }
+              }
+            } else {
+              const int slot = i & 1, o = kWG == 2 ? slot : 0;
+              ok = full(vp) && wait(&p_full[slot], (p_par >> slot) & 1);
+              p_par ^= 1u << slot;
+              if (!ok) break;
+              tc_fence_after();
+              values(slot, o, vp, i == 0 || (kWG == 2 && i == 1));
+              umma_commit(&kv_empty[vp % kNS]);
+              umma_commit(&o_full[slot]);
+              if (i + 2 < n) {
+                const uint32_t kp = n0 + k_place(i + 2);
+                ok = full(kp);
+                if (!ok) break;
+                scores(slot, 0, kp);
+                umma_commit(&kv_empty[kp % kNS]);
+                if (i + 3 == n) umma_commit(&q_empty);
+                umma_commit(&s_full[slot]);
+              }
+            }
+          }
+          n0 += 2 * n;
+        }
+        umma_commit(&drain);  // every MMA and commit before it, in the error case too
+        mbar_wait_bounded(&drain, 0, a.status);
+      }
+      __syncwarp();
     }
   }
   tc_fence_before();
