@@ -47,7 +47,7 @@ namespace {
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kPaOCol = 256;   // first TMEM column of O; S (and P over it) below
 constexpr float kPaRescale = 8.f;   // log2 margin before the running maximum moves
-constexpr int kPaCubicEvery = 4;    // of so many pairs of exponentials, one goes to the FMA pipe
+constexpr int kPaCubicEvery = 1000;    // of so many pairs of exponentials, one goes to the FMA pipe
 constexpr int kPaPieces = 4;        // pieces published at once
 constexpr int kPaBadRing = 16;      // tiles whose missing pages are remembered
 constexpr float kLog2e = 1.4426950408889634f;
@@ -64,7 +64,7 @@ struct Pa {
   // with the static arrays (3 KB, a multiple of the dynamic array's alignment) all of an SM's shared memory for d = 128
   static constexpr int kSmem = kWG * kQBytes + kStages * kStageBytes;
   static constexpr int kSoftmax = kWG * 128;             // softmax threads
-  static constexpr int kThreads = kSoftmax + (kWG == 2 ? 128 : 96);
+  static constexpr int kThreads = kSoftmax + 128;
   static constexpr int kPer = (1024 + kThreads - 1) / kThreads;  // sequences per thread in the prologue
   static constexpr uint32_t kSCols = kTile;              // columns of one S slot (two slots)
 };
@@ -73,7 +73,8 @@ struct PaParams {
   CUtensorMap q, k, v;
   PagedAttnArgs a;
   int G, tpt;      // query heads per KV head; tokens per query tile
-  int box, nbox;   // rows of a TMA box; boxes per tile
+  int box, nbox;   // rows of a TMA box (a power of two); boxes per tile
+  int tile_pages, tile_rows;  // a tile's length in pages and rows
   float scale_log2;
 };
 
@@ -187,23 +188,31 @@ struct Walk {
   }
 };
 
-// Places of a piece's loads in the ring: K_0, K_1, V_0, K_2, V_1, ..., V_{n-1}.
-__device__ __forceinline__ int k_place(int i) { return i == 0 ? 0 : 2 * i - 1; }
-__device__ __forceinline__ int v_place(int i, int n) { return i + 1 < n ? 2 * i + 2 : 2 * n - 1; }
-
 struct Waiter {
   volatile int* dead;
   int* status;
+  // The hint lets a waiting warp sleep in the barrier unit; the clock is read every 64 wake-ups, because
+  // waiting warps share the issue slots with the ones at work.
   __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = global_timer_ns();
-    while (true) {
-      if (mbar_try_wait(bar, parity)) return true;
+    uint64_t t0 = 0;
+    for (uint32_t n = 0;; ++n) {
+      uint32_t done;
+      asm volatile(
+          "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+          " selp.u32 %0, 1, 0, p;\n}\n"
+          : "=r"(done)
+          : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
+          : "memory");
+      if (done) return true;
       if (*dead) return false;
-      if (global_timer_ns() - t0 > kWaitLimitNs) {
-        flag_error(status, DEVFLAG_TIMEOUT);
-        *dead = 1;
-        return false;
+      if (n % 64 == 63) {
+        const uint64_t t = global_timer_ns();
+        if (t0 == 0) t0 = t;
+        if (t - t0 > kWaitLimitNs) {
+          flag_error(status, DEVFLAG_TIMEOUT);
+          *dead = 1;
+          return false;
+        }
       }
     }
   }
@@ -266,16 +275,36 @@ __device__ __forceinline__ uint64_t exp2_cubic2(uint64_t x) {
 // Bits [0, n) of a word, n clamped to [0, 32].
 __device__ __forceinline__ uint32_t bits_below(int n) { return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u); }
 
-// Page of this lane's box of tile i: -2 where the item has no keys, -1 where the table names no page.
+// One box of an item's tiles, from tile to tile: its page-table entry and row within the page.
 template <int D>
-__device__ __forceinline__ int box_page(const PaParams& p, const Piece& s, int i, int box, bool on, int* t_out) {
-  const int v = i * Pa<D>::kTile + box * p.box;
-  if (!on || v >= s.it.nv) return -2;
-  const int t = v < s.it.s_al ? v : v + s.it.shift;
-  *t_out = t;
-  const int pg = __ldg(p.a.table + static_cast<int64_t>(s.b) * p.a.max_pages + t / p.a.pool.page_size);
-  return pg < 0 || pg >= p.a.pool.n_pages ? -1 : pg;
-}
+struct BoxWalk {
+  int v, slot, row;
+  __device__ void place(const PaParams& p, const Item& it) {
+    const int t = v < it.s_al ? v : v + it.shift;
+    slot = t / p.a.pool.page_size;
+    row = t - slot * p.a.pool.page_size;
+  }
+  __device__ BoxWalk(const PaParams& p, const Piece& s, int box) : v(s.t0 * Pa<D>::kTile + box * p.box) {
+    place(p, s.it);
+  }
+  // Page of the box: -2 where the item has no keys, -1 where the table names no page.
+  __device__ int page(const PaParams& p, const Piece& s, bool on) const {
+    if (!on || v >= s.it.nv) return -2;
+    const int pg = __ldg(p.a.table + static_cast<int64_t>(s.b) * p.a.max_pages + slot);
+    return pg < 0 || pg >= p.a.pool.n_pages ? -1 : pg;
+  }
+  __device__ void step(const PaParams& p, const Item& it) {
+    const bool sink = v < it.s_al;
+    v += Pa<D>::kTile;
+    if (sink && v >= it.s_al) {
+      place(p, it);
+    } else {
+      slot += p.tile_pages;
+      row += p.tile_rows;
+      if (row >= p.a.pool.page_size) row -= p.a.pool.page_size, ++slot;
+    }
+  }
+};
 
 // Whether tile i holds rows that no query of the item sees.
 template <int D>
@@ -386,18 +415,19 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 128);
+      mbar_init(&p_full[i], 4);
       mbar_init(&o_full[i], 1);
     }
     for (int i = 0; i < kPaPieces; ++i) {
       mbar_init(&piece_full[i], 1);
-      mbar_init(&piece_empty[i], C::kSoftmax / 32 + 2);
+      mbar_init(&piece_empty[i], C::kSoftmax / 32 + 3);
     }
     mbar_init(&wg_bar, C::kSoftmax);
     mbar_init(&drain, 1);
     fence_mbarrier_init();
   }
-  constexpr int kMmaWarp = kWG * 4, kLoadWarp = kMmaWarp + 1, kZeroWarp = kMmaWarp + 2;
+  constexpr int kMmaWarp = kWG * 4, kLoadWarp = kMmaWarp + 1, kZeroWarp = kMmaWarp + 2,
+                kValueWarp = kMmaWarp + 3;
   if (warp == kMmaWarp) tmem_alloc(&tmem_base_s, kTmemCols);
   tc_fence_before();
   __syncthreads();
@@ -443,6 +473,12 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
     if (*ok && pieces[k % kPaPieces].t1 == 0) *ok = false;
     return pieces[k % kPaPieces];
   };
+  auto all_ok = [&](bool x) { return __all_sync(0xFFFFFFFFu, x) != 0; };
+  auto drain_loads = [&](uint32_t used) {  // after a timeout: each load under way arrives, or has, on one of two barriers
+    for (int i = 0; i < kNS; ++i)
+      if ((used >> i) & 1)
+        for (int t = 0; t < 2; ++t) mbar_wait_bounded(&kv_full[i], t, a.status, 1000000);
+  };
   auto release = [&](int k) {
     __syncwarp();
     if (lane == 0) mbar_arrive(&piece_empty[k % kPaPieces]);
@@ -460,7 +496,6 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
     uint32_t s_par = 0, o_par = 0;    // phases of s_full and o_full, a bit per slot
     uint32_t tiles0 = 0, wg_par = 0;  // tiles before the piece
     bool ok = true;
-    auto all_ok = [&](bool x) { return __all_sync(0xFFFFFFFFu, x) != 0; };
     auto sync_wgs = [&]() {
       mbar_arrive(&wg_bar);
       const bool x = all_ok(wait(&wg_bar, wg_par));
@@ -528,10 +563,12 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
               m = mx;
               l *= alpha;
             }
-            if (!first) {  // the products before this tile have to be done
-              ok = all_ok(wait(&o_full[prev], ((o_par >> prev) & 1) ^ 1));
-              if (!ok) break;
-              tc_fence_after();
+            if (!first) {  // the products before this tile have to be done; with two streams its scores came after them
+              if constexpr (kWG == 1) {
+                ok = all_ok(wait(&o_full[prev], ((o_par >> prev) & 1) ^ 1));
+                if (!ok) break;
+                tc_fence_after();
+              }
 #pragma unroll 1
               for (int c = 0; c < D / 32; ++c) {
                 float v[32];
@@ -549,7 +586,8 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
           auto exponentials = [&](auto cubic) {
 #pragma unroll
             for (int c = 0; c < kTile / 32; ++c) {
-              uint32_t hi[16], lo[16];
+              uint32_t hi[16];
+              [[maybe_unused]] uint32_t lo[16];
 #pragma unroll
               for (int e = 0; e < 16; ++e) {
                 const uint64_t z = fma2(pack2(x[32 * c + 2 * e], x[32 * c + 2 * e + 1]), scale2, mm2);
@@ -583,14 +621,16 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
           tmem_st_wait();
         }
         first = false;
-        o_par ^= 1u << slot;
+        if (kWG == 1) o_par ^= 1u << slot;
         prev = slot;
         tc_fence_before();
-        mbar_arrive(&p_full[slot]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[slot]);
       }
       tiles0 += s.t1 - s.t0;
       if (!ok) break;
       if (!first) {
+        if (kWG == 2) o_par ^= 1u << prev;  // once a piece
         ok = all_ok(wait(&o_full[prev], ((o_par >> prev) & 1) ^ 1));
         if (!ok) break;
       }
@@ -764,22 +804,24 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
   } else {
     if constexpr (kWG == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == kLoadWarp) {
-      // ------------------------------------------------------------------ loads
+      // ------------------------------------------------------------------ pieces, Q and K
       const int box = lane / kDB, db = lane % kDB;
       const bool on = box < p.nbox;
-      uint32_t n = 0, tiles = 0;  // ring places filled; tiles begun
+      uint32_t st = 0, st_par = 1, used = 0, tiles = 0;  // the next stage, its phase before, stages in use; tiles begun
       bool ok = true;
       Walk<D> walk(p, line);
       for (int piece = 0; ok; ++piece) {
         const Piece s = walk.next();
         const int at = piece % kPaPieces;
-        if (piece >= kPaPieces) ok = __all_sync(0xFFFFFFFFu, wait(&piece_empty[at], ((piece / kPaPieces) & 1) ^ 1));
+        if (piece >= kPaPieces) ok = all_ok(wait(&piece_empty[at], ((piece / kPaPieces) & 1) ^ 1));
         if (ok && lane == 0) {
           pieces[at] = s;
           mbar_arrive(&piece_full[at]);
         }
         if (!ok || s.t1 == 0) break;
-        if (piece > 0) ok = __all_sync(0xFFFFFFFFu, wait(&q_empty, (piece - 1) & 1));
+        BoxWalk<D> bw(p, s, box);
+        int pg_next = bw.page(p, s, on);
+        if (piece > 0) ok = all_ok(wait(&q_empty, (piece - 1) & 1));
         if (!ok) break;
         const int nqt = s.it.solo ? 1 : 2;
         if (lane == 0) mbar_arrive_expect_tx(&q_full, nqt * kDB * p.tpt * p.G * 128);
@@ -787,105 +829,135 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
         if (lane < nqt * kDB)
           tma_load_3d(q_s + (lane / kDB) * C::kQBytes + db * C::kQBlock, &p.q, db * 64, s.h * p.G,
                       static_cast<int>(s.q0) + (lane / kDB) * p.tpt, &q_full);
-        int t_next = 0, t_prev = 0, pg_prev = -2;
-        int pg_next = box_page<D>(p, s, s.t0, box, on, &t_next);
-        // step i: K of tile i, V of tile i - 1
-        for (int i = s.t0; ok && i <= s.t1; ++i) {
-          const int pg = pg_next, t = t_next;
-          pg_next = -2;
-          if (i + 1 < s.t1) pg_next = box_page<D>(p, s, i + 1, box, on, &t_next);
-          for (int kv = 0; kv < 2; ++kv) {
-            const bool is_v = kv == 1;
-            if (is_v ? i == s.t0 : i == s.t1) continue;
-            const int pgx = is_v ? pg_prev : pg, tx = is_v ? t_prev : t;
-            const uint32_t st = n % kNS;
-            if (n >= kNS) ok = __all_sync(0xFFFFFFFFu, wait(&kv_empty[st], ((n / kNS) & 1) ^ 1));
-            if (!ok) break;
-            const uint32_t bad = __ballot_sync(0xFFFFFFFFu, pgx == -1);
-            const uint32_t loads = __popc(__ballot_sync(0xFFFFFFFFu, pgx >= 0));
-            uint64_t* bar = &kv_full[st];
-            if (is_v && (bad || edge_tile<D>(s.it, i - 1))) bar = &edge_full[st];
-            if (lane == 0) {
-              if (!is_v) {
-                bad_s[tiles % kPaBadRing] = bad;
-                if (bad) flag_error(a.status, DEVFLAG_BAD_INDEX);
-              }
-              mbar_arrive_expect_tx(bar, loads * p.box * 128);
-            }
-            if (!is_v) ++tiles;
-            __syncwarp();
-            if (pgx >= 0)
-              tma_load_4d(kv_s + st * C::kStageBytes + db * (kTile * 128) + box * p.box * 128, is_v ? &p.v : &p.k,
-                          db * 64, tx % a.pool.page_size, s.h, pgx, bar);
-            ++n;
+        for (int i = s.t0; i < s.t1; ++i) {
+          const int pg = pg_next, row = bw.row;
+          bw.step(p, s.it);
+          pg_next = i + 1 < s.t1 ? bw.page(p, s, on) : -2;  // the next tile's, while this one waits
+          ok = all_ok(wait(&kv_empty[st], st_par));
+          if (!ok) break;
+          const uint32_t bad = __ballot_sync(0xFFFFFFFFu, pg == -1);
+          const uint32_t loads = __popc(__ballot_sync(0xFFFFFFFFu, pg >= 0));
+          if (lane == 0) {
+            bad_s[tiles % kPaBadRing] = bad;
+            if (bad) flag_error(a.status, DEVFLAG_BAD_INDEX);
+            mbar_arrive_expect_tx(&kv_full[st], loads * p.box * 128);
           }
-          pg_prev = pg;
-          t_prev = t;
+          __syncwarp();
+          if (pg >= 0)
+            tma_load_4d(kv_s + st * C::kStageBytes + db * (kTile * 128) + box * p.box * 128, &p.k, db * 64, row, s.h,
+                        pg, &kv_full[st]);
+          used |= 1u << st;
+          st += 2;
+          if (st >= kNS) st -= kNS, st_par ^= 1;
+          ++tiles;
         }
       }
-      if (!ok) {  // wait for the copies in flight
-        if (lane == 0)
-          for (uint32_t i = n > kNS ? n - kNS : 0; i < n; ++i)
-            mbar_wait_bounded(&kv_full[i % kNS], (i / kNS) & 1, a.status);
-      }
-    } else if (warp == kZeroWarp) {
-      // ------------------------------------------------------------------ unseen V rows
-      const int box = lane / kDB;
+      if (dead_s && lane == 0) drain_loads(used);
+    } else if (warp == kValueWarp) {
+      // ------------------------------------------------------------------ V
+      const int box = lane;
       const bool on = box < p.nbox;
-      uint32_t n0 = 0, par = 0;  // ring place of the piece; phase of each edge barrier
+      uint32_t st = 1, st_par = 1, used = 0;
       bool ok = true;
       for (int piece = 0; ok; ++piece) {
         const Piece& s = take(piece, &ok);
         if (!ok) break;
-        const int nt = s.t1 - s.t0;
-        for (int i = s.t0; ok && i < s.t1; ++i) {
-          int t = 0;
-          const uint32_t bad = __ballot_sync(0xFFFFFFFFu, box_page<D>(p, s, i, box, on, &t) == -1);
-          if (!bad && !edge_tile<D>(s.it, i)) continue;
-          const uint32_t st = (n0 + v_place(i - s.t0, nt)) % kNS;
-          ok = __all_sync(0xFFFFFFFFu, wait(&edge_full[st], (par >> st) & 1));
+        BoxWalk<D> bw(p, s, box);
+        int pg_next = bw.page(p, s, on);
+        for (int i = s.t0; i < s.t1; ++i) {
+          const int pg = pg_next, row = bw.row;
+          bw.step(p, s.it);
+          pg_next = i + 1 < s.t1 ? bw.page(p, s, on) : -2;
+          ok = all_ok(wait(&kv_empty[st], st_par));
           if (!ok) break;
-          par ^= 1u << st;
+          const uint32_t bad = __ballot_sync(0xFFFFFFFFu, pg == -1);
+          const uint32_t loads = __popc(__ballot_sync(0xFFFFFFFFu, pg >= 0));
+          uint64_t* bar = bad || edge_tile<D>(s.it, i) ? &edge_full[st] : &kv_full[st];
+          if (lane == 0) mbar_arrive_expect_tx(bar, loads * p.box * (kDB * 128));
+          __syncwarp();
+          if (pg >= 0)
+            tma_load_5d(kv_s + st * C::kStageBytes + box * p.box * (kDB * 128), &p.v, 0, row, 0, s.h, pg, bar);
+          used |= 1u << st;
+          st += 2;
+          if (st >= kNS) st -= kNS, st_par ^= 1;
+        }
+        if (ok) release(piece);
+      }
+      if (dead_s && lane == 0) drain_loads(used);
+    } else if (warp == kZeroWarp) {
+      // ------------------------------------------------------------------ unseen V rows
+      const bool on = lane < p.nbox;
+      uint32_t st = 1, par = 0;  // the next V's stage; phase of each edge barrier
+      bool ok = true;
+      for (int piece = 0; ok; ++piece) {
+        const Piece& s = take(piece, &ok);
+        if (!ok) break;
+        BoxWalk<D> bw(p, s, lane);
+        int pg_next = bw.page(p, s, on);
+        for (int i = s.t0; i < s.t1; ++i) {
+          const uint32_t bad = __ballot_sync(0xFFFFFFFFu, pg_next == -1), here = st;
+          bw.step(p, s.it);
+          pg_next = i + 1 < s.t1 ? bw.page(p, s, on) : -2;
+          st += 2;
+          if (st >= kNS) st -= kNS;
+          if (!bad && !edge_tile<D>(s.it, i)) continue;
+          ok = all_ok(wait(&edge_full[here], (par >> here) & 1));
+          if (!ok) break;
+          par ^= 1u << here;
           for (int r = lane; r < kTile; r += 32) {
-            const int v = i * kTile + r;
-            const bool lost = (bad >> ((r / p.box) * kDB)) & 1;
-            if (lost || v >= s.it.nv || (v >= s.it.z0 && v < s.it.z1)) {
-  #pragma unroll
+            const int v = i * kTile + r, box = r / p.box;
+            if (((bad >> box) & 1) || v >= s.it.nv || (v >= s.it.z0 && v < s.it.z1)) {
+              const uint32_t at = kv_s + here * C::kStageBytes + box * p.box * (kDB * 128) + (r - box * p.box) * 128;
+#pragma unroll
               for (int x = 0; x < kDB * 8; ++x)
-                st_shared_v4(kv_s + st * C::kStageBytes + (x >> 3) * (kTile * 128) + r * 128 + (x & 7) * 16, 0, 0, 0,
-                             0);
+                st_shared_v4(at + (x >> 3) * p.box * 128 + (x & 7) * 16, 0, 0, 0, 0);
             }
           }
-          fence_async_smem();
+        fence_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&kv_full[st]);
+          if (lane == 0) mbar_arrive(&kv_full[here]);
         }
-        n0 += 2 * nt;
-        release(piece);
+        if (ok) release(piece);
       }
     } else if (warp == kMmaWarp) {
       // ------------------------------------------------------------------ MMAs
       if (lane == 0) {
+        // One thread issues everything, so what it does between two MMAs is kept to a few instructions:
+        // descriptors are a low word per stage plus constants, ring places are stepped, not computed.
         const uint32_t idesc_s = instr_desc(128, kTile, false, false);
         const uint32_t idesc_o = instr_desc(128, D, true, false);
-        uint32_t n0 = 0, p_par = 0;  // ring place of the piece; phases of p_full, a bit per slot
+        const uint32_t q_lo = (q_s >> 4) | (1u << 16);
+        const uint32_t k_lo = (kv_s >> 4) | (1u << 16);
+        // V lies box by box: 64-dim blocks a box apart, and a box's 16-key steps of all blocks before the next box's
+        const uint32_t v_lo = (kv_s >> 4) | (static_cast<uint32_t>(p.box * 8) << 16);
+        const int box_shift = 31 - __clz(p.box >> 4), box_skip = (kDB - 1) * p.box * 8;
+        uint32_t p_par = 0;          // phases of p_full, a bit per slot
+        // the ring holds K_0, V_0, K_1, V_1, ...: the next K's and the next V's stage and phase
+        uint32_t ks = 0, k_par = 0, vs = 1, v_par = 0;
         bool ok = true;
-        auto full = [&](uint32_t place) { return wait(&kv_full[place % kNS], (place / kNS) & 1); };
-        auto scores = [&](int slot, int qt, uint32_t place) {
-          const uint32_t qa = q_s + qt * C::kQBytes, ka = kv_s + (place % kNS) * C::kStageBytes;
-  #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            umma_bf16(tmem + slot * C::kSCols, smem_desc(qa + (kk >> 2) * C::kQBlock + (kk & 3) * 32, 16, 1024),
-                      smem_desc(ka + (kk >> 2) * (kTile * 128) + (kk & 3) * 32, 16, 1024), idesc_s, kk != 0);
+        auto next_k = [&]() {
+          ks += 2;
+          if (ks >= kNS) ks -= kNS, k_par ^= 1;
         };
-        auto values = [&](int slot, int o, uint32_t place, bool first) {
-          const uint32_t va = kv_s + (place % kNS) * C::kStageBytes;
-  #pragma unroll
+        auto next_v = [&]() {
+          vs += 2;
+          if (vs >= kNS) vs -= kNS, v_par ^= 1;
+        };
+        auto scores = [&](int slot, int qt, uint32_t stage) {
+          const uint32_t qa = q_lo + qt * (C::kQBytes >> 4), ka = k_lo + stage * (C::kStageBytes >> 4);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            umma_bf16_lo(tmem + slot * C::kSCols, qa + (kk >> 2) * (C::kQBlock >> 4) + (kk & 3) * 2,
+                         ka + (kk >> 2) * (kTile * 128 >> 4) + (kk & 3) * 2, idesc_s, kk != 0);
+        };
+        auto values = [&](int slot, int o, uint32_t stage, bool first) {
+          const uint32_t va = v_lo + stage * (C::kStageBytes >> 4);
+#pragma unroll
           for (int part = 0; part < (F32 ? 2 : 1); ++part)
-  #pragma unroll
+#pragma unroll
             for (int kt = 0; kt < kTile / 16; ++kt)
-              umma_bf16_ts(tmem + kPaOCol + o * D, tmem + slot * C::kSCols + (kt >> 1) * 32 + part * 16 + (kt & 1) * 8,
-                           smem_desc(va + kt * 2048, kTile * 128, 1024), idesc_o, !first || part || kt);
+              umma_bf16_ts_lo(tmem + kPaOCol + o * D, tmem + slot * C::kSCols + (kt >> 1) * 32 + part * 16 + (kt & 1) * 8,
+                              va + kt * (2048 >> 4) + (kt >> box_shift) * box_skip, idesc_o, part || kt ? 1u : !first);
         };
         for (int piece = 0; ok; ++piece) {
           const int at = piece % kPaPieces;
@@ -894,66 +966,84 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
           const int n = pieces[at].t1 - pieces[at].t0;
           const bool pair = !pieces[at].it.solo;
           mbar_arrive(&piece_empty[at]);
-          ok = wait(&q_full, piece & 1) && full(n0);
+          ok = wait(&q_full, piece & 1) && wait(&kv_full[ks], k_par);
           if (!ok) break;
           tc_fence_after();
-          for (int st = 0; st < (pair ? 2 : 1); ++st) {
-            scores(st, st, n0);
-            umma_commit(&s_full[st]);
-          }
-          umma_commit(&kv_empty[n0 % kNS]);
-          if (n == 1) umma_commit(&q_empty);
-          if (!pair && n > 1) {
-            ok = full(n0 + k_place(1));
-            if (!ok) break;
-            scores(1, 0, n0 + k_place(1));
+          scores(0, 0, ks);
+          umma_commit(&s_full[0]);
+          if (pair) {
+            scores(1, 1, ks);
             umma_commit(&s_full[1]);
-            umma_commit(&kv_empty[(n0 + k_place(1)) % kNS]);
-            if (n == 2) umma_commit(&q_empty);
           }
-          for (int i = 0; ok && i < n; ++i) {
-            const uint32_t vp = n0 + v_place(i, n);
-            if (pair) {
-              const uint32_t kp = n0 + k_place(i + 1);
-              ok = (i + 1 == n || full(kp)) && full(vp);
-              for (int st = 0; ok && st < 2; ++st) {
-                ok = wait(&p_full[st], (p_par >> st) & 1);
-                p_par ^= 1u << st;
-                if (!ok) break;
-                tc_fence_after();
-                values(st, st, vp, i == 0);
-                if (st == 1) umma_commit(&kv_empty[vp % kNS]);
-                umma_commit(&o_full[st]);
-                if (i + 1 < n) {
-                  scores(st, st, kp);
-                  if (st == 1) {
-                    umma_commit(&kv_empty[kp % kNS]);
-                    if (i + 2 == n) umma_commit(&q_empty);
-                  }
-                  umma_commit(&s_full[st]);
-                }
-              }
-            } else {
-              const int slot = i & 1, o = kWG == 2 ? slot : 0;
-              ok = full(vp) && wait(&p_full[slot], (p_par >> slot) & 1);
-              p_par ^= 1u << slot;
+          umma_commit(&kv_empty[ks]);
+          if (n == 1) umma_commit(&q_empty);
+          next_k();
+          if (pair) {
+            // a stream's next scores follow its product, so s_full tells its warps too that the product is done
+            for (int i = 0; i < n; ++i) {
+              const bool more = i + 1 < n;
+              ok = wait(&kv_full[vs], v_par) && wait(&p_full[0], p_par & 1);
               if (!ok) break;
               tc_fence_after();
-              values(slot, o, vp, i == 0 || (kWG == 2 && i == 1));
-              umma_commit(&kv_empty[vp % kNS]);
-              umma_commit(&o_full[slot]);
-              if (i + 2 < n) {
-                const uint32_t kp = n0 + k_place(i + 2);
-                ok = full(kp);
+              values(0, 0, vs, i == 0);
+              if (more) {
+                ok = wait(&kv_full[ks], k_par);
                 if (!ok) break;
-                scores(slot, 0, kp);
-                umma_commit(&kv_empty[kp % kNS]);
+                scores(0, 0, ks);
+                umma_commit(&s_full[0]);
+              } else {
+                umma_commit(&o_full[0]);
+              }
+              ok = wait(&p_full[1], p_par >> 1);
+              if (!ok) break;
+              tc_fence_after();
+              values(1, 1, vs, i == 0);
+              umma_commit(&kv_empty[vs]);
+              next_v();
+              if (more) {
+                scores(1, 1, ks);
+                umma_commit(&s_full[1]);
+                umma_commit(&kv_empty[ks]);
+                if (i + 2 == n) umma_commit(&q_empty);
+                next_k();
+              } else {
+                umma_commit(&o_full[1]);
+              }
+              p_par ^= 3;
+            }
+          } else {
+            // tiles take turns with the slots
+            if (n > 1) {
+              ok = wait(&kv_full[ks], k_par);
+              if (!ok) break;
+              scores(1, 0, ks);
+              umma_commit(&s_full[1]);
+              umma_commit(&kv_empty[ks]);
+              if (n == 2) umma_commit(&q_empty);
+              next_k();
+            }
+            for (int i = 0; i < n; ++i) {
+              const int slot = i & 1, o = kWG == 2 ? slot : 0;
+              const bool more = i + 2 < n;
+              ok = wait(&kv_full[vs], v_par) && wait(&p_full[slot], (p_par >> slot) & 1);
+              if (!ok) break;
+              p_par ^= 1u << slot;
+              tc_fence_after();
+              values(slot, o, vs, i == 0 || (kWG == 2 && i == 1));
+              umma_commit(&kv_empty[vs]);
+              if (kWG == 1 || !more) umma_commit(&o_full[slot]);
+              next_v();
+              if (more) {
+                ok = wait(&kv_full[ks], k_par);
+                if (!ok) break;
+                scores(slot, 0, ks);
+                umma_commit(&kv_empty[ks]);
                 if (i + 3 == n) umma_commit(&q_empty);
                 umma_commit(&s_full[slot]);
+                next_k();
               }
             }
           }
-          n0 += 2 * n;
         }
         umma_commit(&drain);  // every MMA and commit before it, in the error case too
         mbar_wait_bounded(&drain, 0, a.status);
@@ -989,8 +1079,8 @@ EncodeTiled encode_tiled() {
 // Map of a bf16 tensor whose innermost extent is d (boxes of 64 of them, 128-byte swizzle).  The
 // stride of an extent of 1 is never used and set to a row's, which the encoder accepts.
 bool encode(CUtensorMap* m, const void* base, int rank, const int64_t* extent, const int64_t* stride, const int* box) {
-  cuuint64_t dims[4], strides[3];
-  cuuint32_t boxes[4], ones[4] = {1, 1, 1, 1};
+  cuuint64_t dims[5], strides[4];
+  cuuint32_t boxes[5], ones[5] = {1, 1, 1, 1, 1};
   for (int i = 0; i < rank; ++i) {
     dims[i] = static_cast<cuuint64_t>(extent[i]);
     boxes[i] = static_cast<cuuint32_t>(box[i]);
@@ -1012,15 +1102,20 @@ cudaError_t launch(const PagedAttnArgs& a, int num_sms, cudaStream_t s) {
   p.box = 16;  // the largest power of two that divides a page, at most a tile
   while (p.box < C::kTile && a.pool.page_size % (2 * p.box) == 0) p.box *= 2;
   p.nbox = C::kTile / p.box;
+  p.tile_pages = C::kTile / a.pool.page_size;
+  p.tile_rows = C::kTile % a.pool.page_size;
   p.scale_log2 = a.sm_scale * kLog2e;
   const int64_t qe[3] = {D, a.Hq, a.n_tokens}, qs[3] = {1, D, a.q_stride};
   const int qb[3] = {64, p.G, p.tpt};
   const int64_t ke[4] = {D, a.pool.page_size, a.pool.Hkv, a.pool.n_pages};
   const int64_t ks[4] = {1, a.pool.ks[2], a.pool.ks[1], a.pool.ks[0]};
-  const int64_t vs[4] = {1, a.pool.vs[2], a.pool.vs[1], a.pool.vs[0]};
   const int kb[4] = {64, p.box, 1, 1};
+  // V's 64-dim blocks are a dimension of their own: one box brings all of a row
+  const int64_t ve[5] = {64, a.pool.page_size, C::kDB, a.pool.Hkv, a.pool.n_pages};
+  const int64_t vs[5] = {1, a.pool.vs[2], 64, a.pool.vs[1], a.pool.vs[0]};
+  const int vb[5] = {64, p.box, C::kDB, 1, 1};
   if (!encode(&p.q, a.Q, 3, qe, qs, qb) || !encode(&p.k, a.pool.K, 4, ke, ks, kb) ||
-      !encode(&p.v, a.pool.V, 4, ke, vs, kb))
+      !encode(&p.v, a.pool.V, 5, ve, vs, vb))
     return cudaErrorInvalidValue;
   auto kernel = paged_attn_kernel<D, F32>;
   static int done[64] = {0};
