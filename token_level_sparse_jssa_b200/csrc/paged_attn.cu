@@ -810,8 +810,18 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
       uint32_t st = 0, st_par = 1, used = 0, tiles = 0;  // the next stage, its phase before, stages in use; tiles begun
       bool ok = true;
       Walk<D> walk(p, line);
+      Piece late;     // the rest of an item that an earlier CTA began comes last: the CTAs then go through
+      late.t1 = 0;    // the keys of one head side by side, and find them in L2
       for (int piece = 0; ok; ++piece) {
-        const Piece s = walk.next();
+        Piece s = walk.next();
+        if (piece == 0 && s.t1 > 0 && s.t0 > 0) {
+          late = s;
+          s = walk.next();
+        }
+        if (s.t1 == 0) {
+          s = late;
+          late.t1 = 0;
+        }
         const int at = piece % kPaPieces;
         if (piece >= kPaPieces) ok = all_ok(wait(&piece_empty[at], ((piece / kPaPieces) & 1) ^ 1));
         if (ok && lane == 0) {
