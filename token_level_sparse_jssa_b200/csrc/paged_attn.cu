@@ -47,7 +47,7 @@ namespace {
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kPaOCol = 256;   // first TMEM column of O; S (and P over it) below
 constexpr float kPaRescale = 8.f;   // log2 margin before the running maximum moves
-constexpr int kPaCubicEvery = 1000;    // of so many pairs of exponentials, one goes to the FMA pipe
+constexpr int kPaCubicEvery = 8;    // of so many pairs of exponentials, one goes to the FMA pipe
 constexpr int kPaPieces = 4;        // pieces published at once
 constexpr int kPaBadRing = 16;      // tiles whose missing pages are remembered
 constexpr float kLog2e = 1.4426950408889634f;
@@ -113,7 +113,7 @@ __device__ __forceinline__ Item item_at(const PaParams& p, int nq, int len, int 
 
 // An item's length on the line: a tile of two query tiles counts twice, and what a piece costs
 // before its first tile and after its last stands at the front.
-constexpr int kPaItemUnits = 2;
+constexpr int kPaItemUnits = 8;
 __device__ __forceinline__ int64_t item_units(const Item& it) {
   return kPaItemUnits + (it.solo ? it.ntiles : 2 * static_cast<int64_t>(it.ntiles));
 }
