@@ -65,7 +65,6 @@ struct Pa {
   static constexpr int kSmem = kWG * kQBytes + kStages * kStageBytes;
   static constexpr int kSoftmax = kWG * 128;             // softmax threads
   static constexpr int kThreads = kSoftmax + 128;
-  static constexpr int kPer = (1024 + kThreads - 1) / kThreads;  // sequences per thread in the prologue
   static constexpr uint32_t kSCols = kTile;              // columns of one S slot (two slots)
 };
 
@@ -118,10 +117,21 @@ __device__ __forceinline__ int64_t item_units(const Item& it) {
   return kPaItemUnits + (it.solo ? it.ntiles : 2 * static_cast<int64_t>(it.ntiles));
 }
 
-// The CTAs' cuts of the line and this CTA's first item, written once by the prologue.
-struct Line {
-  int64_t total, seq_start, per_head, start;
-  int nact, b, h, j;
+// Quotient of non-negative numbers, on the 32-bit path where both fit.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
+// The cuts of the line: CTA c has [start(c), start(c + 1)).
+struct Cuts {
+  int64_t len, more;  // `more` CTAs have len + 1 units
+  __device__ Cuts(int64_t total, int n) : len(quotient(total, n)), more(total - len * n) {}
+  __device__ int64_t start(int c) const { return c * len + min64(c, more); }
+  __device__ int owner(int64_t x) const {  // of place x
+    const int64_t y = x - more * (len + 1);
+    return static_cast<int>(y < 0 ? quotient(x, len + 1) : more + quotient(y, len));
+  }
 };
 
 // A CTA's share of one item: tiles [t0, t1); t1 = 0 ends the CTA's work.  CTAs c_first to c_last share the item.
@@ -135,16 +145,14 @@ struct Piece {
 template <int D>
 struct Walk {
   const PaParams& p;
-  int64_t u, u0, u1, total, q0;
-  int nact, b, h, j, nq, len;
+  Cuts cuts;
+  int64_t u, u0, u1, q0;
+  int b, h, j, nq, len;
 
-  __device__ Walk(const PaParams& pp, const Line& s) : p(pp) {
-    total = s.total;
-    nact = s.nact;
-    u0 = blockIdx.x * total / nact;
-    u1 = (blockIdx.x + 1) * total / nact;
-    u = s.start;
-    b = s.b, h = s.h, j = s.j;
+  __device__ Walk(const PaParams& pp, const Cuts& cc, int64_t start, int b0, int h0, int j0)
+      : p(pp), cuts(cc), u(start), b(b0), h(h0), j(j0) {
+    u0 = cuts.start(blockIdx.x);
+    u1 = cuts.start(blockIdx.x + 1);
     load();
   }
   __device__ void load() {
@@ -153,7 +161,6 @@ struct Walk {
                                    p.a.max_q_len, nullptr);
     q0 = t.q0, nq = t.nq, len = t.len;
   }
-  __device__ int owner(int64_t x) const { return static_cast<int>(((x + 1) * nact + total - 1) / total) - 1; }
   __device__ Piece next() {
     Piece c;
     c.t1 = 0;
@@ -177,9 +184,9 @@ struct Walk {
         }
       }
       if (c.t0 < c.t1) {
-        c.c_first = c.t0 == 0 ? static_cast<int>(blockIdx.x) : owner(at);
+        c.c_first = at >= u0 ? static_cast<int>(blockIdx.x) : cuts.owner(at);
         c.c_last = c.t1 == c.it.ntiles ? static_cast<int>(blockIdx.x)
-                                       : owner(at + static_cast<int64_t>(w) * (c.it.ntiles - 1));
+                                       : cuts.owner(at + static_cast<int64_t>(w) * (c.it.ntiles - 1));
         return c;
       }
       c.t1 = 0;
@@ -334,11 +341,9 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
   using C = Pa<D>;
   constexpr int kTile = C::kTile, kWG = C::kWG, kDB = C::kDB, kNS = C::kStages;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t q_full, q_empty, kv_full[kNS], kv_empty[kNS], edge_full[kNS], s_full[2], p_full[2],
+  __shared__ __align__(8) uint64_t q_full, q_empty, kv_full[kNS], kv_empty[kNS], edge_full[kNS], s_full[2], p_half[2], p_full[2],
       o_full[2], piece_full[kPaPieces], piece_empty[kPaPieces], wg_bar, drain;
-  __shared__ Piece pieces[kPaPieces];
-  __shared__ Line line;
-  __shared__ int64_t warp_sum[C::kThreads / 32];
+  __shared__ Piece pieces[kPaPieces], late_piece;
   __shared__ uint32_t tmem_base_s, bad_s[kPaBadRing];
   __shared__ float ml_s[2][2][128];  // solo items: each warpgroup's maxima and sums
   __shared__ int dead_s, last_s;
@@ -353,56 +358,25 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
     prefetch_tensormap(&p.v);
   }
 
-  // ---- the line: every CTA adds up all sequences' items (a few consecutive ones per thread)
-  int64_t mine = 0, units[C::kPer];
-  const int per = (a.B + C::kThreads - 1) / C::kThreads;
-#pragma unroll
-  for (int e = 0; e < C::kPer; ++e) {
-    units[e] = 0;
-    const int b = tid * per + e;
-    if (e < per && b < a.B) {
+  // ---- each sequence's length on the line (per KV head), into the ring, which is still empty
+  int64_t* seq_units = reinterpret_cast<int64_t*>(smem_raw + kWG * C::kQBytes);
+  {
+    // a warp per sequence where sequences may have many items, a thread otherwise
+    const int tpi = p.tpt * kWG;
+    const bool wide = a.max_q_len > 8 * tpi;
+    const int step = wide ? C::kThreads / 32 : C::kThreads;
+    for (int b = wide ? warp : tid; b < a.B; b += step) {
       const NewTokens t = new_tokens(a.q_begin, a.seq_lens, b, cap, a.n_tokens, a.max_q_len,
                                      blockIdx.x == 0 ? a.status : nullptr);
-      for (int j = 0, at = 0; at < t.nq; ++j) {
-        const Item it = item_at<D>(p, t.nq, t.len, j);
-        units[e] += item_units(it);
-        at += it.ntok;
+      int64_t n = 0;
+      for (int j = wide ? lane : 0; j * static_cast<int64_t>(tpi) < t.nq; j += wide ? 32 : 1)
+        n += item_units(item_at<D>(p, t.nq, t.len, j));
+      if (wide) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
       }
+      if (!wide || lane == 0) seq_units[b] = n;
     }
-    mine += units[e] * a.pool.Hkv;
-  }
-  int64_t inc = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-    if (lane >= o) inc += v;
-  }
-  if (lane == 31) warp_sum[warp] = inc;
-  __syncthreads();
-  int64_t before = inc - mine, total = 0;
-#pragma unroll
-  for (int w = 0; w < C::kThreads / 32; ++w) {
-    if (w < warp) before += warp_sum[w];
-    total += warp_sum[w];
-  }
-  // at least two units per CTA, so that each cut piece has a whole tile
-  const int nact = static_cast<int>(min64(gridDim.x, max64(1, total / 2)));
-  if (total == 0 || static_cast<int>(blockIdx.x) >= nact) return;
-  const int64_t u0 = blockIdx.x * total / nact;
-  if (u0 >= before && u0 < before + mine) {
-    int64_t at = before;
-#pragma unroll
-    for (int e = 0; e < C::kPer; ++e) {
-      const int64_t n = units[e] * a.pool.Hkv;
-      if (u0 >= at && u0 < at + n) {
-        line.b = tid * per + e;
-        line.seq_start = at;
-        line.per_head = units[e];
-      }
-      at += n;
-    }
-    line.total = total;
-    line.nact = nact;
   }
   if (tid == 0) {
     dead_s = 0;
@@ -415,6 +389,7 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
+      mbar_init(&p_half[i], 4);
       mbar_init(&p_full[i], 4);
       mbar_init(&o_full[i], 1);
     }
@@ -429,40 +404,10 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
   constexpr int kMmaWarp = kWG * 4, kLoadWarp = kMmaWarp + 1, kZeroWarp = kMmaWarp + 2,
                 kValueWarp = kMmaWarp + 3;
   if (warp == kMmaWarp) tmem_alloc(&tmem_base_s, kTmemCols);
+  fence_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 0) {  // this CTA's first item within its sequence
-    const NewTokens t = new_tokens(a.q_begin, a.seq_lens, line.b, cap, a.n_tokens, a.max_q_len, nullptr);
-    int64_t rem = u0 - line.seq_start;
-    const int h = static_cast<int>(rem / line.per_head);
-    rem -= h * line.per_head;
-    int64_t at = u0 - rem;
-    const int tpi = p.tpt * kWG;
-    for (int j0 = 0; j0 * static_cast<int64_t>(tpi) < t.nq; j0 += 32) {
-      const int j = j0 + lane;
-      const int64_t n = j * static_cast<int64_t>(tpi) < t.nq ? item_units(item_at<D>(p, t.nq, t.len, j)) : 0;
-      int64_t s = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xFFFFFFFFu, s, o);
-        if (lane >= o) s += v;
-      }
-      const int64_t all = __shfl_sync(0xFFFFFFFFu, s, 31);
-      if (rem < all) {
-        if (rem >= s - n && rem < s) {
-          line.h = h;
-          line.j = j;
-          line.start = at + s - n;
-        }
-        break;
-      }
-      rem -= all;
-      at += all;
-    }
-  }
-  __syncthreads();
-
   const uint32_t tmem = tmem_base_s;
   const uint32_t base = smem_u32(smem_raw);
   const uint32_t q_s = base, kv_s = base + kWG * C::kQBytes;
@@ -583,42 +528,47 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
           const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2), mm2 = pack2(-mm, -mm);
           uint64_t l2[2] = {0, 0};
           // P over the scores it comes from: in the first 16 of 32 columns, its remainder in the other 16
-          auto exponentials = [&](auto cubic) {
+          // (the cubic takes a masked score for 2^-126, which no fp32 sum notices; a row without keys is told by m)
+          constexpr bool kCubic = !F32 && kWG == 2;
 #pragma unroll
-            for (int c = 0; c < kTile / 32; ++c) {
-              uint32_t hi[16];
-              [[maybe_unused]] uint32_t lo[16];
+          for (int c = 0; c < kTile / 32; ++c) {
+            uint32_t hi[16];
+            [[maybe_unused]] uint32_t lo[16];
 #pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const uint64_t z = fma2(pack2(x[32 * c + 2 * e], x[32 * c + 2 * e + 1]), scale2, mm2);
-                float p0, p1;
-                uint64_t pp;
-                if (cubic && e % kPaCubicEvery == kPaCubicEvery - 1) {
-                  pp = exp2_cubic2(z);
-                  unpack2(pp, p0, p1);
-                } else {
-                  unpack2(z, p0, p1);
-                  p0 = exp2_approx(p0);
-                  p1 = exp2_approx(p1);
-                  pp = pack2(p0, p1);
-                }
-                l2[e & 1] = add2(l2[e & 1], pp);
-                hi[e] = pack_bf16x2(p0, p1);
-                if constexpr (F32)
-                  lo[e] =
-                      pack_bf16x2(p0 - bf16_bits_to_float(hi[e] & 0xFFFFu), p1 - __uint_as_float(hi[e] & 0xFFFF0000u));
+            for (int e = 0; e < 16; ++e) {
+              const uint64_t z = fma2(pack2(x[32 * c + 2 * e], x[32 * c + 2 * e + 1]), scale2, mm2);
+              float p0, p1;
+              uint64_t pp;
+              if (kCubic && e % kPaCubicEvery == kPaCubicEvery - 1) {
+                pp = exp2_cubic2(z);
+                unpack2(pp, p0, p1);
+              } else {
+                unpack2(z, p0, p1);
+                p0 = exp2_approx(p0);
+                p1 = exp2_approx(p1);
+                pp = pack2(p0, p1);
               }
-              tmem_st16_nowait(s_col + 32 * c, hi);
-              if constexpr (F32) tmem_st16_nowait(s_col + 32 * c + 16, lo);
+              l2[e & 1] = add2(l2[e & 1], pp);
+              hi[e] = pack_bf16x2(p0, p1);
+              if constexpr (F32)
+                lo[e] =
+                    pack_bf16x2(p0 - bf16_bits_to_float(hi[e] & 0xFFFFu), p1 - __uint_as_float(hi[e] & 0xFFFF0000u));
             }
-          };
-          // the cubic takes -infinity for 2^-126, which masked scores must not be
-          if (F32 || kWG == 1 || masked) exponentials(std::false_type());
-          else exponentials(std::true_type());
+            if (c == kTile / 64) {  // the first half of P is stored: its product can begin
+              tmem_st_wait();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&p_half[slot]);
+            }
+            tmem_st16_nowait(s_col + 32 * c, hi);
+            if constexpr (F32) tmem_st16_nowait(s_col + 32 * c + 16, lo);
+          }
           float la, lb;
           unpack2(add2(l2[0], l2[1]), la, lb);
           l += la + lb;
           tmem_st_wait();
+        } else if (lane == 0) {
+          mbar_arrive(&p_half[slot]);
         }
         first = false;
         if (kWG == 1) o_par ^= 1u << slot;
@@ -634,6 +584,7 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
         ok = all_ok(wait(&o_full[prev], ((o_par >> prev) & 1) ^ 1));
         if (!ok) break;
       }
+      if (m == -INFINITY) l = 0.f;
       // the row's factor on each accumulator that holds a share of it
       float f0 = 1.f, f1 = 0.f;
       if (split_keys) {
@@ -809,26 +760,91 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
       const bool on = box < p.nbox;
       uint32_t st = 0, st_par = 1, used = 0, tiles = 0;  // the next stage, its phase before, stages in use; tiles begun
       bool ok = true;
-      Walk<D> walk(p, line);
-      Piece late;     // the rest of an item that an earlier CTA began comes last: the CTAs then go through
-      late.t1 = 0;    // the keys of one head side by side, and find them in L2
+      // the line's length, and the item that this CTA's stretch of it begins in
+      const int per = (a.B + 31) / 32;
+      int64_t mine = 0;
+      for (int e = 0; e < per && lane * per + e < a.B; ++e) mine += seq_units[lane * per + e] * a.pool.Hkv;
+      int64_t before = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xFFFFFFFFu, before, o);
+        if (lane >= o) before += v;
+      }
+      const int64_t total = __shfl_sync(0xFFFFFFFFu, before, 31);
+      before -= mine;
+      // at least two units per CTA, so that each cut piece has a whole tile
+      const int nact = static_cast<int>(min64(gridDim.x, max64(1, total / 2)));
+      const Cuts cuts(total, nact);
+      const bool idle = total == 0 || static_cast<int>(blockIdx.x) >= nact;
+      int64_t at = 0;
+      int b0 = 0, h0 = 0, j0 = 0;
+      if (!idle) {
+        const int64_t u0 = cuts.start(blockIdx.x);
+        const uint32_t owner = __ballot_sync(0xFFFFFFFFu, u0 >= before && u0 < before + mine);
+        const int from = __ffs(owner) - 1;
+        at = before;
+        b0 = lane * per;
+        if (lane == from)
+          while (u0 >= at + seq_units[b0] * a.pool.Hkv) at += seq_units[b0++] * a.pool.Hkv;
+        at = __shfl_sync(0xFFFFFFFFu, at, from);
+        b0 = __shfl_sync(0xFFFFFFFFu, b0, from);
+        const int64_t per_head = seq_units[b0];
+        h0 = static_cast<int>(quotient(u0 - at, per_head));
+        at += h0 * per_head;
+        int64_t rem = u0 - at;
+        const NewTokens t = new_tokens(a.q_begin, a.seq_lens, b0, cap, a.n_tokens, a.max_q_len, nullptr);
+        for (;; j0 += 32) {
+          const int64_t tok = (j0 + lane) * static_cast<int64_t>(p.tpt * kWG);
+          const int64_t n = tok < t.nq ? item_units(item_at<D>(p, t.nq, t.len, j0 + lane)) : 0;
+          int64_t sum = n;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+            if (lane >= o) sum += v;
+          }
+          const uint32_t past = __ballot_sync(0xFFFFFFFFu, sum > rem);
+          if (past) {
+            const int l0 = __ffs(past) - 1;
+            j0 += l0;
+            at += __shfl_sync(0xFFFFFFFFu, sum - n, l0);
+            break;
+          }
+          const int64_t all = __shfl_sync(0xFFFFFFFFu, sum, 31);
+          rem -= all;
+          at += all;
+        }
+      }
+      __syncwarp();  // seq_units has been read; loads write there next
+      fence_async_smem();
+      Walk<D> walk(p, cuts, at, b0, h0, j0);
+      if (idle) walk.u = walk.u1 = 0;
+      // The rest of an item that an earlier CTA began comes last: the CTAs of a head then go through its
+      // keys side by side, and find them in L2.
+      bool late = false;
       for (int piece = 0; ok; ++piece) {
-        Piece s = walk.next();
-        if (piece == 0 && s.t1 > 0 && s.t0 > 0) {
-          late = s;
-          s = walk.next();
-        }
-        if (s.t1 == 0) {
-          s = late;
-          late.t1 = 0;
-        }
         const int at = piece % kPaPieces;
         if (piece >= kPaPieces) ok = all_ok(wait(&piece_empty[at], ((piece / kPaPieces) & 1) ^ 1));
-        if (ok && lane == 0) {
-          pieces[at] = s;
-          mbar_arrive(&piece_full[at]);
+        if (!ok) break;
+        {
+          Piece c = walk.next();
+          if (piece == 0 && c.t1 > 0 && c.t0 > 0) {
+            late = true;
+            if (lane == 0) late_piece = c;
+            __syncwarp();
+            c = walk.next();
+          }
+          if (c.t1 == 0 && late) {
+            late = false;
+            c = late_piece;
+          }
+          if (lane == 0) {
+            pieces[at] = c;
+            mbar_arrive(&piece_full[at]);
+          }
+          __syncwarp();
         }
-        if (!ok || s.t1 == 0) break;
+        const Piece& s = pieces[at];
+        if (s.t1 == 0) break;
         BoxWalk<D> bw(p, s, box);
         int pg_next = bw.page(p, s, on);
         if (piece > 0) ok = all_ok(wait(&q_empty, (piece - 1) & 1));
@@ -960,12 +976,12 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
             umma_bf16_lo(tmem + slot * C::kSCols, qa + (kk >> 2) * (C::kQBlock >> 4) + (kk & 3) * 2,
                          ka + (kk >> 2) * (kTile * 128 >> 4) + (kk & 3) * 2, idesc_s, kk != 0);
         };
-        auto values = [&](int slot, int o, uint32_t stage, bool first) {
+        auto values = [&](int slot, int o, uint32_t stage, bool first, int k0, int k1) {
           const uint32_t va = v_lo + stage * (C::kStageBytes >> 4);
 #pragma unroll
           for (int part = 0; part < (F32 ? 2 : 1); ++part)
 #pragma unroll
-            for (int kt = 0; kt < kTile / 16; ++kt)
+            for (int kt = k0; kt < k1; ++kt)
               umma_bf16_ts_lo(tmem + kPaOCol + o * D, tmem + slot * C::kSCols + (kt >> 1) * 32 + part * 16 + (kt & 1) * 8,
                               va + kt * (2048 >> 4) + (kt >> box_shift) * box_skip, idesc_o, part || kt ? 1u : !first);
         };
@@ -992,10 +1008,14 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
             // a stream's next scores follow its product, so s_full tells its warps too that the product is done
             for (int i = 0; i < n; ++i) {
               const bool more = i + 1 < n;
-              ok = wait(&kv_full[vs], v_par) && wait(&p_full[0], p_par & 1);
+              ok = wait(&kv_full[vs], v_par) && wait(&p_half[0], p_par & 1);
               if (!ok) break;
               tc_fence_after();
-              values(0, 0, vs, i == 0);
+              values(0, 0, vs, i == 0, 0, kTile / 32);
+              ok = wait(&p_full[0], p_par & 1);
+              if (!ok) break;
+              tc_fence_after();
+              values(0, 0, vs, false, kTile / 32, kTile / 16);
               if (more) {
                 ok = wait(&kv_full[ks], k_par);
                 if (!ok) break;
@@ -1004,10 +1024,14 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
               } else {
                 umma_commit(&o_full[0]);
               }
+              ok = wait(&p_half[1], p_par >> 1);
+              if (!ok) break;
+              tc_fence_after();
+              values(1, 1, vs, i == 0, 0, kTile / 32);
               ok = wait(&p_full[1], p_par >> 1);
               if (!ok) break;
               tc_fence_after();
-              values(1, 1, vs, i == 0);
+              values(1, 1, vs, false, kTile / 32, kTile / 16);
               umma_commit(&kv_empty[vs]);
               next_v();
               if (more) {
@@ -1039,7 +1063,7 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
               if (!ok) break;
               p_par ^= 1u << slot;
               tc_fence_after();
-              values(slot, o, vs, i == 0 || (kWG == 2 && i == 1));
+              values(slot, o, vs, i == 0 || (kWG == 2 && i == 1), 0, kTile / 16);
               umma_commit(&kv_empty[vs]);
               if (kWG == 1 || !more) umma_commit(&o_full[slot]);
               next_v();
