@@ -313,7 +313,7 @@ __device__ __forceinline__ int64_t pool_vec(const int64_t (&st)[3], int page_siz
 
 // A block takes chunks of 256 x kCopyPer vectors of one pool of one pair; every thread's loads are
 // issued before its stores.
-constexpr int kCopyPer = 8;
+constexpr int kCopyPer = 4;
 __global__ void __launch_bounds__(256) pages_copy_kernel(PagePool p, const int32_t* src, const int32_t* dst, int n,
                                                          const int32_t* count, int* status) {
   if (count) n = max(0, min(n, count[0]));
@@ -368,8 +368,9 @@ __device__ __forceinline__ int append_place(const PagedAppendArgs& a, int64_t i,
   return p;
 }
 
-// A block takes kAppendTokens tokens: their places first, then their vectors.
-constexpr int kAppendTokens = 4;
+// A block takes kAppendTokens tokens: their places first, then their vectors, four loads of a
+// thread under way before its first store.
+constexpr int kAppendTokens = 8, kAppendPer = 4;
 __global__ void __launch_bounds__(256) paged_append_kernel(PagedAppendArgs a) {
   __shared__ int page_s[kAppendTokens], row_s[kAppendTokens];
   const int64_t i0 = static_cast<int64_t>(blockIdx.x) * kAppendTokens;
@@ -379,18 +380,27 @@ __global__ void __launch_bounds__(256) paged_append_kernel(PagedAppendArgs a) {
     row_s[threadIdx.x] = row;
   }
   __syncthreads();
-  const int cpr = a.pool.d / 8, per = a.pool.Hkv * cpr;
-  for (int v = threadIdx.x; v < kAppendTokens * 2 * per; v += 256) {
-    const int j = v / (2 * per), rest = v - j * 2 * per;
-    const int p = page_s[j];
-    if (p < 0) continue;
-    const bool is_v = rest >= per;
-    const int e = is_v ? rest - per : rest;
-    const int64_t(&st)[3] = is_v ? a.pool.vs : a.pool.ks;
-    const uint4* from = reinterpret_cast<const uint4*>(is_v ? a.V_new : a.K_new) + (i0 + j) * (a.new_stride >> 3) + e;
-    uint4* to = reinterpret_cast<uint4*>(is_v ? a.pool.V : a.pool.K) + p * (st[0] >> 3) +
-                (e / cpr) * (st[1] >> 3) + row_s[j] * (st[2] >> 3) + e % cpr;
-    *to = *from;
+  const int cpr = a.pool.d / 8, per = a.pool.Hkv * cpr;  // 16-byte vectors of a row, of a token's K or V rows
+  const int total = kAppendTokens * 2 * per;
+  for (int v0 = threadIdx.x; v0 < total; v0 += 256 * kAppendPer) {
+    uint4 x[kAppendPer];
+    uint4* to[kAppendPer];
+#pragma unroll
+    for (int u = 0; u < kAppendPer; ++u) {
+      const int v = v0 + u * 256;
+      const int j = v / (2 * per), rest = v - j * 2 * per;
+      to[u] = nullptr;
+      if (v >= total || page_s[j] < 0) continue;
+      const bool is_v = rest >= per;
+      const int e = is_v ? rest - per : rest;
+      const int64_t(&st)[3] = is_v ? a.pool.vs : a.pool.ks;
+      x[u] = __ldcs(reinterpret_cast<const uint4*>(is_v ? a.V_new : a.K_new) + (i0 + j) * (a.new_stride >> 3) + e);
+      to[u] = reinterpret_cast<uint4*>(is_v ? a.pool.V : a.pool.K) + page_s[j] * (st[0] >> 3) + (e / cpr) * (st[1] >> 3) +
+              row_s[j] * (st[2] >> 3) + e % cpr;
+    }
+#pragma unroll
+    for (int u = 0; u < kAppendPer; ++u)
+      if (to[u]) *to[u] = x[u];
   }
 }
 
@@ -423,7 +433,7 @@ cudaError_t launch_pages_compact(const PageBook& k, int32_t* src, int32_t* dst, 
 cudaError_t launch_pages_copy(const PagePool& p, const int32_t* src, const int32_t* dst, int n, const int32_t* count,
                               int* status, int num_sms, cudaStream_t s) {
   const int64_t chunks = ceil_div(static_cast<int64_t>(p.Hkv) * p.page_size * (p.d / 8), 256 * kCopyPer);
-  const int64_t blocks = min64(static_cast<int64_t>(n) * 2 * chunks, static_cast<int64_t>(num_sms) * 8);
+  const int64_t blocks = min64(static_cast<int64_t>(n) * 2 * chunks, static_cast<int64_t>(num_sms) * 64);
   return launch_ex(pages_copy_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, 0, p, src, dst, n, count,
                    status);
 }
