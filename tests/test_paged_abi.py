@@ -174,3 +174,21 @@ def test_host_tensors_are_refused():
                  lambda: jssa.pages_copy(L, K, V, n, n, None, n)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_a_changed_layout_is_seen(monkeypatch):
+    # what a call derives from a layout's fields follows the fields' present values
+    import token_level_sparse_jssa_b200 as jssa
+    from token_level_sparse_jssa_b200 import _paged
+    monkeypatch.setattr(_paged, "_device", lambda: -1)      # where host tensors say they are
+    K, V = torch.zeros(2, 6, 2, 16, 64, dtype=torch.bfloat16)
+    L = jssa.make_paged_layout(K, V, torch.zeros(3, 4, dtype=torch.int32), 8)
+    assert _paged._pool(K, _paged._facts(L).pool, _paged._facts(L).k_stride, "K", -1) == K.data_ptr()
+    L.n_pages = 5
+    L.k_stride[0] = 4096
+    f = _paged._facts(L)
+    assert f.pool == (5, 2, 16, 64) and f.k_stride == (4096, 1024, 64, 1)
+    with pytest.raises(ValueError):
+        _paged._pool(K, f.pool, f.k_stride, "K", -1)
+    with pytest.raises(ValueError):
+        _paged._pool(K[:5], f.pool, f.k_stride, "K", -1)

@@ -38,8 +38,29 @@ def _signatures():
 _b.SIGNATURE_SOURCES.append(_signatures)
 
 
-# A decode step makes several of these calls, each on a few microseconds of GPU work, so the checks
-# below read every property of a tensor once and leave the wording of a refusal to _refuse().
+# A decode step makes several of these calls, each on a few microseconds of GPU work.  So the checks
+# below read every property of a tensor once, what follows from a layout's fields is derived once
+# for their present values, and the wording of a refusal is left to _refuse().
+class _Facts:
+    __slots__ = ("fields", "heads", "pool", "k_stride", "v_stride", "table", "ref", "seq", "begin", "out")
+
+    def __init__(self, L, fields):
+        self.fields = fields
+        self.heads = L.Hq, L.Hkv, L.d
+        self.pool = L.n_pages, L.Hkv, L.page_size, L.d
+        self.k_stride, self.v_stride = tuple(L.k_stride) + (1,), tuple(L.v_stride) + (1,)
+        self.table, self.ref, self.seq, self.begin = (L.B, L.max_pages), (L.n_pages,), (L.B,), (L.B + 1,)
+        self.out = torch.bfloat16 if L.out_dtype == OUT_BF16 else torch.float32
+
+
+def _facts(L):
+    fields = bytes(L)
+    f = L.__dict__.get("facts")
+    if f is None or f.fields != fields:
+        f = L.__dict__["facts"] = _Facts(L, fields)
+    return f
+
+
 def _refuse(t, what, dev, expected):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{what}: device tensor expected")
@@ -72,16 +93,13 @@ def _list(t, what, dev):
     return _packed(t, torch.int32, (n,), what, dev), n
 
 
-def _pools(L, K, V, dev):
-    shape = (L.n_pages, L.Hkv, L.page_size, L.d)
-    for t, strides, what in ((K, L.k_stride[:], "K"), (V, L.v_stride[:], "V")):
-        if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype is not torch.bfloat16 or \
-                t.shape != shape:
-            _refuse(t, what, dev, f"bfloat16 pool {shape}")
-        a, b, c, one = t.stride()
-        if one != 1 or [a, b, c] != strides and any(n > 1 and x != y for n, x, y in zip(shape, (a, b, c), strides)):
-            _refuse(t, what, dev, f"the layout's strides {strides}")
-    return K.data_ptr(), V.data_ptr()
+def _pool(t, shape, strides, what, dev):
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype is not torch.bfloat16 or t.shape != shape:
+        _refuse(t, what, dev, f"bfloat16 pool {shape}")
+    got = t.stride()
+    if got != strides and (got[3] != 1 or any(n > 1 and x != y for n, x, y in zip(shape, got, strides))):
+        _refuse(t, what, dev, f"the layout's strides {strides}")
+    return t.data_ptr()
 
 
 def _rows(t, heads, d, what, dev):
@@ -95,13 +113,10 @@ def _rows(t, heads, d, what, dev):
     return t.data_ptr(), n, (row if n > 1 else heads * d)
 
 
-def _table(L, page_table, dev):
-    return _packed(page_table, torch.int32, (L.B, L.max_pages), "page_table", dev)
-
-
-def _book(L, page_table, ref_count, seq_lens, dev):
-    return (_table(L, page_table, dev), _packed(ref_count, torch.int32, (L.n_pages,), "ref_count", dev),
-            _packed(seq_lens, torch.int32, (L.B,), "seq_lens", dev))
+def _book(f, page_table, ref_count, seq_lens, dev):
+    return (_packed(page_table, torch.int32, f.table, "page_table", dev),
+            _packed(ref_count, torch.int32, f.ref, "ref_count", dev),
+            _packed(seq_lens, torch.int32, f.seq, "seq_lens", dev))
 
 
 def _ws(ws, dev):
@@ -109,7 +124,7 @@ def _ws(ws, dev):
         return None, 0
     if not isinstance(ws, torch.Tensor) or ws.get_device() != dev:
         _refuse(ws, "ws", dev, "workspace")
-    return ws.data_ptr(), ws.numel() * ws.element_size()
+    return ws.data_ptr(), ws.nbytes
 
 
 def make_paged_layout(K: torch.Tensor, V: torch.Tensor, page_table: torch.Tensor, Hq: int,
@@ -144,84 +159,96 @@ def alloc_paged_workspace(L: PagedLayout, max_q_len: int = 0, device=None) -> to
 
 def paged_append_kv(L, K_new, V_new, K, V, page_table, q_begin, seq_lens, ws, stream=None):
     """Write the newest tokens' rows K_new, V_new [n_tokens, Hkv, d] into their pages."""
-    dev, H, d, B = _device(), L.Hkv, L.d, L.B
+    dev, f = _device(), _facts(L)
+    _, H, d = f.heads
     k, nk, ks = _rows(K_new, H, d, "K_new", dev)
     v, nv, vs = _rows(V_new, H, d, "V_new", dev)
     if nk != nv or ks != vs:
         raise ValueError("K_new and V_new must have the same rows and row stride")
+    w, nw = _ws(ws, dev)
     code = load().jssa_paged_append_kv(
-        C.byref(L), k, v, ks, nk, *_pools(L, K, V, dev), _table(L, page_table, dev),
-        _packed(q_begin, torch.int32, (B + 1,), "q_begin", dev), _packed(seq_lens, torch.int32, (B,), "seq_lens", dev),
-        *_ws(ws, dev), _stream(stream, dev))
-    _check("jssa_paged_append_kv", code)
+        C.byref(L), k, v, ks, nk, _pool(K, f.pool, f.k_stride, "K", dev), _pool(V, f.pool, f.v_stride, "V", dev),
+        _packed(page_table, torch.int32, f.table, "page_table", dev),
+        _packed(q_begin, torch.int32, f.begin, "q_begin", dev), _packed(seq_lens, torch.int32, f.seq, "seq_lens", dev),
+        w, nw, _stream(stream, dev))
+    if code:
+        _check("jssa_paged_append_kv", code)
 
 
 def paged_attn(L, Q, K, V, page_table, q_begin, max_q_len: int, seq_lens, window: int, n_sinks: int, sm_scale: float,
                O, lse=None, ws=None, stream=None):
     """Causal attention of the newest tokens Q [n_tokens, Hq, d] over their sequences' pages, with
     an optional sliding window (window > 0) and n_sinks first tokens that stay visible."""
-    dev, Hq, d, B = _device(), L.Hq, L.d, L.B
+    dev, f = _device(), _facts(L)
+    Hq, _, d = f.heads
     q, n, qs = _rows(Q, Hq, d, "Q", dev)
+    w, nw = _ws(ws, dev)
     code = load().jssa_paged_attn(
-        C.byref(L), q, qs, n, max_q_len, *_pools(L, K, V, dev), _table(L, page_table, dev),
-        _packed(q_begin, torch.int32, (B + 1,), "q_begin", dev), _packed(seq_lens, torch.int32, (B,), "seq_lens", dev),
-        window, n_sinks, sm_scale,
-        _packed(O, torch.bfloat16 if L.out_dtype == OUT_BF16 else torch.float32, (n, Hq, d), "O", dev),
-        None if lse is None else _packed(lse, torch.float32, (n, Hq), "lse", dev), *_ws(ws, dev),
-        _stream(stream, dev))
-    _check("jssa_paged_attn", code)
+        C.byref(L), q, qs, n, max_q_len, _pool(K, f.pool, f.k_stride, "K", dev),
+        _pool(V, f.pool, f.v_stride, "V", dev), _packed(page_table, torch.int32, f.table, "page_table", dev),
+        _packed(q_begin, torch.int32, f.begin, "q_begin", dev), _packed(seq_lens, torch.int32, f.seq, "seq_lens", dev),
+        window, n_sinks, sm_scale, _packed(O, f.out, (n, Hq, d), "O", dev),
+        None if lse is None else _packed(lse, torch.float32, (n, Hq), "lse", dev), w, nw, _stream(stream, dev))
+    if code:
+        _check("jssa_paged_attn", code)
 
 
 def pages_fork(L, src, dst, page_table, ref_count, seq_lens, ws, stream=None):
     """Sequence dst[i] (empty) becomes a copy of sequence src[i] that shares its pages."""
-    dev = _device()
+    dev, f = _device(), _facts(L)
     s, n = _list(src, "src", dev)
     code = load().jssa_pages_fork(
         C.byref(L), s, _packed(dst, torch.int32, (n,), "dst", dev), n,
-        *_book(L, page_table, ref_count, seq_lens, dev), *_ws(ws, dev), _stream(stream, dev))
-    _check("jssa_pages_fork", code)
+        *_book(f, page_table, ref_count, seq_lens, dev), *_ws(ws, dev), _stream(stream, dev))
+    if code:
+        _check("jssa_pages_fork", code)
 
 
 def pages_reserve(L, n_new, page_table, ref_count, seq_lens, copy_src, copy_dst, ws, stream=None):
     """Room for n_new[b] more tokens of every sequence, added to seq_lens; copy_src/copy_dst [B]
     name the shared pages to copy (pages_copy) before the append."""
-    dev, B = _device(), (L.B,)
+    dev, f = _device(), _facts(L)
     code = load().jssa_pages_reserve(
-        C.byref(L), _packed(n_new, torch.int32, B, "n_new", dev), *_book(L, page_table, ref_count, seq_lens, dev),
-        _packed(copy_src, torch.int32, B, "copy_src", dev), _packed(copy_dst, torch.int32, B, "copy_dst", dev),
+        C.byref(L), _packed(n_new, torch.int32, f.seq, "n_new", dev), *_book(f, page_table, ref_count, seq_lens, dev),
+        _packed(copy_src, torch.int32, f.seq, "copy_src", dev), _packed(copy_dst, torch.int32, f.seq, "copy_dst", dev),
         *_ws(ws, dev), _stream(stream, dev))
-    _check("jssa_pages_reserve", code)
+    if code:
+        _check("jssa_pages_reserve", code)
 
 
 def pages_release(L, ended, window: int, n_sinks: int, page_table, ref_count, seq_lens, ws, stream=None):
     """Give up all pages of the sequences with ended[b] != 0 and, with window > 0, the others' pages
     behind their last `window` tokens that hold none of the first n_sinks."""
-    dev = _device()
+    dev, f = _device(), _facts(L)
     code = load().jssa_pages_release(
-        C.byref(L), None if ended is None else _packed(ended, torch.int32, (L.B,), "ended", dev), window, n_sinks,
-        *_book(L, page_table, ref_count, seq_lens, dev), *_ws(ws, dev), _stream(stream, dev))
-    _check("jssa_pages_release", code)
+        C.byref(L), None if ended is None else _packed(ended, torch.int32, f.seq, "ended", dev), window, n_sinks,
+        *_book(f, page_table, ref_count, seq_lens, dev), *_ws(ws, dev), _stream(stream, dev))
+    if code:
+        _check("jssa_pages_release", code)
 
 
 def pages_compact(L, page_table, ref_count, src, dst, n_moves, ws, stream=None):
     """Move the pages in use to the front of the pool (at most len(src) of them): the table and the
     counts now, the rows with pages_copy(..., src, dst, n_moves)."""
-    dev = _device()
+    dev, f = _device(), _facts(L)
     s, n = _list(src, "src", dev)
     code = load().jssa_pages_compact(
-        C.byref(L), _table(L, page_table, dev), _packed(ref_count, torch.int32, (L.n_pages,), "ref_count", dev), s,
-        _packed(dst, torch.int32, (n,), "dst", dev), n, _packed(n_moves, torch.int32, (1,), "n_moves", dev),
-        *_ws(ws, dev), _stream(stream, dev))
-    _check("jssa_pages_compact", code)
+        C.byref(L), _packed(page_table, torch.int32, f.table, "page_table", dev),
+        _packed(ref_count, torch.int32, f.ref, "ref_count", dev), s, _packed(dst, torch.int32, (n,), "dst", dev), n,
+        _packed(n_moves, torch.int32, (1,), "n_moves", dev), *_ws(ws, dev), _stream(stream, dev))
+    if code:
+        _check("jssa_pages_compact", code)
 
 
 def pages_copy(L, K, V, src, dst, count=None, ws=None, stream=None):
     """Copy page src[i] over page dst[i] in both pools, for every entry or the first count[0];
     negative entries are skipped."""
-    dev = _device()
+    dev, f = _device(), _facts(L)
     s, n = _list(src, "src", dev)
     code = load().jssa_pages_copy(
-        C.byref(L), *_pools(L, K, V, dev), s, _packed(dst, torch.int32, (n,), "dst", dev), n,
+        C.byref(L), _pool(K, f.pool, f.k_stride, "K", dev), _pool(V, f.pool, f.v_stride, "V", dev), s,
+        _packed(dst, torch.int32, (n,), "dst", dev), n,
         None if count is None else _packed(count, torch.int32, (1,), "count", dev), *_ws(ws, dev),
         _stream(stream, dev))
-    _check("jssa_pages_copy", code)
+    if code:
+        _check("jssa_pages_copy", code)
