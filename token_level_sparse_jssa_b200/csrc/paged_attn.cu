@@ -336,6 +336,97 @@ __device__ __forceinline__ void store_out32(void* O, int64_t at, const float (&v
   }
 }
 
+// Merges the pieces of a cut item in their order: the softmax threads of the CTA that finishes it
+// last.  A thread takes kWords 16-byte words of rows at a time and kParts partials of each at once;
+// with fewer words than threads, 2^sh neighbouring lanes share a word's partials.
+template <int D, bool F32, int kWords, int kParts>
+__device__ __forceinline__ void merge_words(const PaParams& p, const Piece& s, int words, int sh) {
+  const PagedAttnArgs& a = p.a;
+  const int n = s.c_last - s.c_first + 1, part = threadIdx.x & ((1 << sh) - 1), wstep = Pa<D>::kSoftmax >> sh;
+  for (int w0 = 0; w0 < words; w0 += kWords * wstep) {
+    float4 o[kWords];
+    float M[kWords], L[kWords];
+    int row[kWords], col[kWords];
+#pragma unroll
+    for (int x = 0; x < kWords; ++x) {
+      const int idx = w0 + x * wstep + (threadIdx.x >> sh);
+      row[x] = idx < words ? idx / (D / 4) : -1;
+      col[x] = idx % (D / 4);
+      o[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+      M[x] = -INFINITY;
+      L[x] = 0.f;
+    }
+    for (int k0 = part; k0 < n; k0 += kParts << sh) {
+      float2 ml[kWords][kParts];
+      float4 v[kWords][kParts];
+#pragma unroll
+      for (int x = 0; x < kWords; ++x)
+#pragma unroll
+        for (int y = 0; y < kParts; ++y) {
+          const int k = k0 + (y << sh);
+          ml[x][y] = make_float2(-INFINITY, 0.f);
+          v[x][y] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (row[x] < 0 || k >= n) continue;
+          // an item's first piece is the last of its CTA, the others the first of theirs
+          const int64_t at = static_cast<int64_t>(2 * (s.c_first + k) + (k == 0 ? 1 : 0)) * a.rows_cap + row[x];
+          ml[x][y] = __ldcg(&a.part_ml[at]);
+          v[x][y] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * D) + col[x]);
+        }
+#pragma unroll
+      for (int x = 0; x < kWords; ++x) {
+        float mn = M[x];
+#pragma unroll
+        for (int y = 0; y < kParts; ++y) mn = fmaxf(mn, ml[x][y].x);  // a piece without keys has m = -infinity
+        const float z = mn == -INFINITY ? 0.f : mn * p.scale_log2;
+        const float w = exp2_approx(fmaf(M[x], p.scale_log2, -z));
+        M[x] = mn;
+        L[x] *= w;
+        o[x].x *= w, o[x].y *= w, o[x].z *= w, o[x].w *= w;
+#pragma unroll
+        for (int y = 0; y < kParts; ++y) {
+          const float u = exp2_approx(fmaf(ml[x][y].x, p.scale_log2, -z));
+          L[x] = fmaf(u, ml[x][y].y, L[x]);
+          o[x].x = fmaf(u, v[x][y].x, o[x].x), o[x].y = fmaf(u, v[x][y].y, o[x].y);
+          o[x].z = fmaf(u, v[x][y].z, o[x].z), o[x].w = fmaf(u, v[x][y].w, o[x].w);
+        }
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < kWords; ++x) {
+      for (int y = 1; y < 1 << sh; y <<= 1) {
+        const float m2 = __shfl_xor_sync(0xFFFFFFFFu, M[x], y), l2 = __shfl_xor_sync(0xFFFFFFFFu, L[x], y);
+        const float mn = fmaxf(M[x], m2), z = mn == -INFINITY ? 0.f : mn * p.scale_log2;
+        const float w1 = exp2_approx(fmaf(M[x], p.scale_log2, -z)), w2 = exp2_approx(fmaf(m2, p.scale_log2, -z));
+        M[x] = mn;
+        L[x] = w1 * L[x] + w2 * l2;
+        o[x].x = w1 * o[x].x + w2 * __shfl_xor_sync(0xFFFFFFFFu, o[x].x, y);
+        o[x].y = w1 * o[x].y + w2 * __shfl_xor_sync(0xFFFFFFFFu, o[x].y, y);
+        o[x].z = w1 * o[x].z + w2 * __shfl_xor_sync(0xFFFFFFFFu, o[x].z, y);
+        o[x].w = w1 * o[x].w + w2 * __shfl_xor_sync(0xFFFFFFFFu, o[x].w, y);
+      }
+      if (part != 0 || row[x] < 0) continue;
+      const float g = L[x] > 0.f ? 1.f / L[x] : 0.f;
+      o[x].x *= g, o[x].y *= g, o[x].z *= g, o[x].w *= g;
+      const int64_t to = (s.q0 + row[x] / p.G) * a.Hq + s.h * p.G + row[x] % p.G;
+      if constexpr (F32)
+        reinterpret_cast<float4*>(static_cast<float*>(a.O) + to * D)[col[x]] = o[x];
+      else
+        reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.O) + to * D)[col[x]] =
+            make_uint2(pack_bf16x2(o[x].x, o[x].y), pack_bf16x2(o[x].z, o[x].w));
+      if (col[x] == 0 && a.lse) a.lse[to] = L[x] > 0.f ? M[x] * a.sm_scale + logf(L[x]) : -INFINITY;
+    }
+  }
+}
+
+template <int D, bool F32>
+__device__ __forceinline__ void merge_pieces(const PaParams& p, const Piece& s) {
+  const int words = s.it.ntok * p.G * (D / 4);
+  int sh = 0;
+  while (sh < 5 && (words << (sh + 1)) <= Pa<D>::kSoftmax) ++sh;
+  if (words > Pa<D>::kSoftmax) merge_words<D, F32, 4, 2>(p, s, words, 0);
+  else merge_words<D, F32, 1, 8>(p, s, words, sh);
+}
+
 template <int D, bool F32>
 __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __grid_constant__ PaParams p) {
   using C = Pa<D>;
@@ -638,12 +729,13 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
         release(piece);
         continue;
       }
-      // ---- the last CTA of a cut item merges its pieces
-      __threadfence();
+      // ---- the last CTA of a cut item merges its pieces (the barrier orders the warps' partials before
+      // thread 0's fence, which orders them before its count)
       ok = sync_wgs();
       if (!ok) break;
       if (tid == 0) {
         const int n = s.c_last - s.c_first + 1;
+        __threadfence();
         const bool last = atomicAdd(a.counters + s.c_first, 1) == n - 1;
         if (last) a.counters[s.c_first] = 0;
         __threadfence();
@@ -651,105 +743,7 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
       }
       ok = sync_wgs();
       if (!ok) break;
-      if (last_s) {
-        __threadfence();
-        const int n = s.c_last - s.c_first + 1;
-        const int rows = s.it.ntok * p.G;
-        // partial k of a row; the first piece of an item is the last of its CTA, the others the first of theirs
-        auto at = [&](int k, int row) {
-          return static_cast<int64_t>(2 * (s.c_first + k) + (k == 0 ? 1 : 0)) * a.rows_cap + row;
-        };
-        // each row's maximum and 1 / sum: a thread per row, or a warp where there are few
-        float* row_m = &ml_s[0][0][0];
-        float* row_g = row_m + C::kSoftmax;
-        const bool by_warp = rows <= 4 * (C::kSoftmax / 32);
-        for (int rr = by_warp ? warp : tid; rr < rows; rr += by_warp ? C::kSoftmax / 32 : C::kSoftmax) {
-          float M = -INFINITY, L = 0.f;
-          const int k0 = by_warp ? lane : 0, kstep = by_warp ? 32 : 1;
-#pragma unroll 4
-          for (int k = k0; k < n; k += kstep) {
-            const float2 ml = __ldcg(&a.part_ml[at(k, rr)]);
-            const float mn = fmaxf(M, ml.x);
-            if (ml.y > 0.f) {
-              L = L * exp2_approx((M - mn) * p.scale_log2) + ml.y * exp2_approx((ml.x - mn) * p.scale_log2);
-              M = mn;
-            }
-          }
-          if (by_warp) {
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-              const float m2 = __shfl_xor_sync(0xFFFFFFFFu, M, o), l2 = __shfl_xor_sync(0xFFFFFFFFu, L, o);
-              const float mn = fmaxf(M, m2);
-              L = (L > 0.f ? L * exp2_approx((M - mn) * p.scale_log2) : 0.f) +
-                  (l2 > 0.f ? l2 * exp2_approx((m2 - mn) * p.scale_log2) : 0.f);
-              M = mn;
-            }
-          }
-          if (!by_warp || lane == 0) {
-            row_m[rr] = M;
-            row_g[rr] = L > 0.f ? 1.f / L : 0.f;
-            if (a.lse)
-              a.lse[(s.q0 + rr / p.G) * a.Hq + s.h * p.G + rr % p.G] = L > 0.f ? M * a.sm_scale + logf(L) : -INFINITY;
-          }
-        }
-        ok = sync_wgs();
-        if (!ok) break;
-        // sums over the partials; with fewer 16-byte words than threads, 2^sh lanes share a word
-        const int words = rows * (D / 4);
-        int sh = 0;
-        while (sh < 5 && (words << (sh + 1)) <= C::kSoftmax) ++sh;
-        const int part = tid & ((1 << sh) - 1), wstep = C::kSoftmax >> sh;
-        constexpr int kBatch = 4;  // words of a thread under way at once
-        for (int w0 = 0; w0 < words; w0 += kBatch * wstep) {
-          float4 o[kBatch];
-          float wm[kBatch], wg2[kBatch];
-          int rr[kBatch], c[kBatch];
-#pragma unroll
-          for (int x = 0; x < kBatch; ++x) {
-            const int idx = w0 + x * wstep + (tid >> sh);
-            rr[x] = idx < words ? idx / (D / 4) : -1;
-            c[x] = idx % (D / 4);
-            wm[x] = row_m[max(rr[x], 0)] * p.scale_log2;
-            wg2[x] = row_g[max(rr[x], 0)];
-            o[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-          }
-          for (int k = part; k < n; k += 1 << sh) {
-            float2 ml[kBatch];
-            float4 v[kBatch];
-#pragma unroll
-            for (int x = 0; x < kBatch; ++x) {
-              if (rr[x] < 0) continue;
-              ml[x] = __ldcg(&a.part_ml[at(k, rr[x])]);
-              v[x] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at(k, rr[x]) * D) + c[x]);
-            }
-#pragma unroll
-            for (int x = 0; x < kBatch; ++x) {
-              if (rr[x] < 0) continue;
-              const float w = ml[x].y > 0.f ? wg2[x] * exp2_approx(fmaf(ml[x].x, p.scale_log2, -wm[x])) : 0.f;
-              o[x].x = fmaf(w, v[x].x, o[x].x), o[x].y = fmaf(w, v[x].y, o[x].y);
-              o[x].z = fmaf(w, v[x].z, o[x].z), o[x].w = fmaf(w, v[x].w, o[x].w);
-            }
-          }
-#pragma unroll
-          for (int x = 0; x < kBatch; ++x) {
-            for (int y = 1; y < 1 << sh; y <<= 1) {
-              o[x].x += __shfl_xor_sync(0xFFFFFFFFu, o[x].x, y);
-              o[x].y += __shfl_xor_sync(0xFFFFFFFFu, o[x].y, y);
-              o[x].z += __shfl_xor_sync(0xFFFFFFFFu, o[x].z, y);
-              o[x].w += __shfl_xor_sync(0xFFFFFFFFu, o[x].w, y);
-            }
-            if (part == 0 && rr[x] >= 0) {
-              const int64_t to = (s.q0 + rr[x] / p.G) * a.Hq + s.h * p.G + rr[x] % p.G;
-              if constexpr (F32)
-                reinterpret_cast<float4*>(static_cast<float*>(a.O) + to * D)[c[x]] = o[x];
-              else
-                reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.O) + to * D)[c[x]] =
-                    make_uint2(pack_bf16x2(o[x].x, o[x].y), pack_bf16x2(o[x].z, o[x].w));
-            }
-          }
-        }
-        ok = sync_wgs();  // row_m and row_g are ml_s
-      }
+      if (last_s) merge_pieces<D, F32>(p, s);
       release(piece);
     }
   } else {
