@@ -240,6 +240,41 @@ def test_binding_refuses_tensors_that_do_not_fit():
             jssa.paged_attn(p.L, **{**args, **kw})
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_pools_inside_one_tensor(d):
+    # K and V of a page side by side in one tensor, rows with room behind them
+    p = Problem([700, 45, 300], [130, 1, 5], d=d, Hkv=2, G=2, page=32)
+    both = torch.full((p.n_pages, 2, 2, 32, d + 8), float("nan"), dtype=torch.bfloat16, device="cuda")
+    K, V = both[:, 0, :, :, :d], both[:, 1, :, :, 8:]
+    assert V.data_ptr() % 16 == 0
+    K.copy_(p.K)
+    V.copy_(p.V)
+    p.K, p.V = K, V
+    p.L = jssa.make_paged_layout(K, V, p.table, p.Hq, jssa.OUT_BF16)
+    p.run()
+    p.check()
+    new = torch.randn(136, 2, d, device="cuda").to(torch.bfloat16)
+    jssa.paged_append_kv(p.L, new, new, K, V, p.table, p.q_begin, p.seq_lens, p.ws)
+    for b in range(3):
+        t = p.pos[b]
+        at = p.table[b].long()[t // 32]
+        assert torch.equal(K[at, :, t % 32], new[p.begin[b]:p.begin[b + 1]])
+        assert torch.equal(V[at, :, t % 32], new[p.begin[b]:p.begin[b + 1]])
+    assert bool(both[:, 0, :, :, d:].isnan().all()) and bool(both[:, 1, :, :, :8].isnan().all())
+
+
+def test_many_pieces_and_many_sequences():
+    # one item cut over the whole GPU; more sequences than the GPU has multiprocessors, most of one tile
+    p = Problem([40000], [1], Hkv=1, G=2, page=64, out=torch.float32)
+    p.run()
+    p.check()
+    r = random.Random(5)
+    lens = [r.choice((1, 3, 60, 129, 400)) for _ in range(1024)]
+    p = Problem(lens, [min(n, r.choice((0, 1, 1, 2))) for n in lens], d=64, Hkv=1, G=4, page=16)
+    p.run()
+    p.check()
+
+
 # --------------------------------------------------------------------------- append
 @pytest.mark.parametrize("nhd", [False, True])
 @pytest.mark.parametrize("d,Hkv,page", [(64, 1, 16), (128, 3, 48), (256, 2, 128)])
@@ -290,7 +325,8 @@ def _same(book, table, ref, lens):
 
 
 @pytest.mark.parametrize("seed,B,mp,n_pages,ps", [(1, 5, 6, 20, 16), (2, 40, 9, 150, 32), (3, 300, 4, 900, 16),
-                                                  (4, 1024, 3, 2500, 16), (5, 64, 40, 33000, 16), (6, 1, 1, 1, 16)])
+                                                  (4, 1024, 3, 2500, 16), (5, 64, 40, 33000, 16), (6, 1, 1, 1, 16),
+                                                  (7, 1000, 70, 9000, 16)])
 def test_page_operations_follow_the_model(seed, B, mp, n_pages, ps):
     r = random.Random(seed)
     book = Book(B, mp, n_pages, ps)
@@ -522,6 +558,20 @@ def test_captured_and_replayed_and_on_another_stream():
         torch.cuda.synchronize()
         assert torch.equal(p.O, want)
     p.check()
+    # two graphs that share a workspace, replayed in turn
+    q = Problem([3000, 10], [1, 10], page=32, window=400, sinks=4, seed=9)
+    q.ws = p.ws = max(p.ws, q.ws, key=len)
+    q.run()
+    graph2 = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph2, stream=side):
+        q.run()
+    with torch.cuda.graph(graph := torch.cuda.CUDAGraph(), stream=side):
+        p.run()
+    for _ in range(3):
+        graph.replay()
+        graph2.replay()
+    p.check()
+    q.check()
     # two calls at once, each with a workspace of its own
     a, b = Problem([5000], [1], seed=2), Problem([900], [300], seed=3)
     s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()

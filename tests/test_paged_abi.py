@@ -87,7 +87,7 @@ def test_attention_arguments(lib):
     for kw in (dict(q=None), dict(o=None), dict(k=None), dict(v=None), dict(table=None), dict(qb=None), dict(sl=None),
                dict(q=FAKE + 8), dict(o=FAKE + 4), dict(lse=FAKE + 2), dict(stride=1023), dict(stride=1028),
                dict(stride=1 << 40), dict(n=-1), dict(n=1 << 31), dict(max_q=-1), dict(window=-1), dict(sinks=-1),
-               dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf"))):
+               dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=2.5e38)):
         assert _attn(lib, L, **kw) == 1, kw
     assert _attn(lib, L, n=0, q=None, o=None, ws=None) == 0
     assert _attn(lib, L, max_q=0, q=None, o=None, ws=None) == 0

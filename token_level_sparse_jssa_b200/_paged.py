@@ -8,9 +8,12 @@ from __future__ import annotations
 import ctypes as C
 
 import torch
+from torch import Tensor
 
 from . import _binding as _b
 from ._binding import OUT_BF16, OUT_F32, _check, load, workspace_init
+
+_I32, _BF16, _F32 = torch.int32, torch.bfloat16, torch.float32
 
 
 class PagedLayout(C.Structure):
@@ -50,7 +53,7 @@ class _Facts:
         self.pool = L.n_pages, L.Hkv, L.page_size, L.d
         self.k_stride, self.v_stride = tuple(L.k_stride) + (1,), tuple(L.v_stride) + (1,)
         self.table, self.ref, self.seq, self.begin = (L.B, L.max_pages), (L.n_pages,), (L.B,), (L.B + 1,)
-        self.out = torch.bfloat16 if L.out_dtype == OUT_BF16 else torch.float32
+        self.out = _BF16 if L.out_dtype == OUT_BF16 else _F32
 
 
 def _facts(L):
@@ -62,7 +65,7 @@ def _facts(L):
 
 
 def _refuse(t, what, dev, expected):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not isinstance(t, Tensor) or not t.is_cuda:
         raise ValueError(f"{what}: device tensor expected")
     if t.get_device() != dev:
         raise ValueError(f"{what} is on {t.device}, not on the current device")
@@ -81,7 +84,7 @@ def _stream(stream, dev):
 
 def _packed(t, dtype, shape, what, dev):
     """Pointer of a contiguous device tensor of the given type and shape."""
-    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype is not dtype or t.shape != shape or \
+    if not isinstance(t, Tensor) or t.get_device() != dev or t.dtype is not dtype or t.shape != shape or \
             not t.is_contiguous():
         _refuse(t, what, dev, f"contiguous {dtype} tensor of shape {shape}")
     return t.data_ptr()
@@ -89,12 +92,12 @@ def _packed(t, dtype, shape, what, dev):
 
 def _list(t, what, dev):
     """(pointer, length) of a contiguous int32 device tensor of one dimension."""
-    n = t.numel() if isinstance(t, torch.Tensor) else 0
-    return _packed(t, torch.int32, (n,), what, dev), n
+    n = t.numel() if isinstance(t, Tensor) else 0
+    return _packed(t, _I32, (n,), what, dev), n
 
 
 def _pool(t, shape, strides, what, dev):
-    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype is not torch.bfloat16 or t.shape != shape:
+    if not isinstance(t, Tensor) or t.get_device() != dev or t.dtype is not _BF16 or t.shape != shape:
         _refuse(t, what, dev, f"bfloat16 pool {shape}")
     got = t.stride()
     if got != strides and (got[3] != 1 or any(n > 1 and x != y for n, x, y in zip(shape, got, strides))):
@@ -104,7 +107,7 @@ def _pool(t, shape, strides, what, dev):
 
 def _rows(t, heads, d, what, dev):
     """(pointer, rows, row stride) of packed token rows [n, heads, d], each row's heads contiguous."""
-    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype is not torch.bfloat16 or t.dim() != 3:
+    if not isinstance(t, Tensor) or t.get_device() != dev or t.dtype is not _BF16 or t.dim() != 3:
         _refuse(t, what, dev, f"bfloat16 rows [n, {heads}, {d}]")
     n, h, e = t.shape
     row, head, one = t.stride()
@@ -114,15 +117,15 @@ def _rows(t, heads, d, what, dev):
 
 
 def _book(f, page_table, ref_count, seq_lens, dev):
-    return (_packed(page_table, torch.int32, f.table, "page_table", dev),
-            _packed(ref_count, torch.int32, f.ref, "ref_count", dev),
-            _packed(seq_lens, torch.int32, f.seq, "seq_lens", dev))
+    return (_packed(page_table, _I32, f.table, "page_table", dev),
+            _packed(ref_count, _I32, f.ref, "ref_count", dev),
+            _packed(seq_lens, _I32, f.seq, "seq_lens", dev))
 
 
 def _ws(ws, dev):
     if ws is None:
         return None, 0
-    if not isinstance(ws, torch.Tensor) or ws.get_device() != dev:
+    if not isinstance(ws, Tensor) or ws.get_device() != dev:
         _refuse(ws, "ws", dev, "workspace")
     return ws.data_ptr(), ws.nbytes
 
@@ -131,7 +134,7 @@ def make_paged_layout(K: torch.Tensor, V: torch.Tensor, page_table: torch.Tensor
                       out_dtype: int = OUT_F32) -> PagedLayout:
     """Layout from pools K and V [n_pages, Hkv, page_size, d] (any strides with a contiguous last
     dimension) and the page table [B, max_pages].  A contiguous cache [B, Hkv, T_cap, d] is a
-    pool of B pages; its table is torch.arange(B, dtype=torch.int32)[:, None]."""
+    pool of B pages; its table is torch.arange(B, dtype=_I32)[:, None]."""
     if K.dim() != 4 or K.shape != V.shape or page_table.dim() != 2:
         raise ValueError("K and V [n_pages, Hkv, page_size, d] and page_table [B, max_pages] expected")
     L = PagedLayout()
@@ -168,8 +171,8 @@ def paged_append_kv(L, K_new, V_new, K, V, page_table, q_begin, seq_lens, ws, st
     w, nw = _ws(ws, dev)
     code = load().jssa_paged_append_kv(
         C.byref(L), k, v, ks, nk, _pool(K, f.pool, f.k_stride, "K", dev), _pool(V, f.pool, f.v_stride, "V", dev),
-        _packed(page_table, torch.int32, f.table, "page_table", dev),
-        _packed(q_begin, torch.int32, f.begin, "q_begin", dev), _packed(seq_lens, torch.int32, f.seq, "seq_lens", dev),
+        _packed(page_table, _I32, f.table, "page_table", dev),
+        _packed(q_begin, _I32, f.begin, "q_begin", dev), _packed(seq_lens, _I32, f.seq, "seq_lens", dev),
         w, nw, _stream(stream, dev))
     if code:
         _check("jssa_paged_append_kv", code)
@@ -185,10 +188,10 @@ def paged_attn(L, Q, K, V, page_table, q_begin, max_q_len: int, seq_lens, window
     w, nw = _ws(ws, dev)
     code = load().jssa_paged_attn(
         C.byref(L), q, qs, n, max_q_len, _pool(K, f.pool, f.k_stride, "K", dev),
-        _pool(V, f.pool, f.v_stride, "V", dev), _packed(page_table, torch.int32, f.table, "page_table", dev),
-        _packed(q_begin, torch.int32, f.begin, "q_begin", dev), _packed(seq_lens, torch.int32, f.seq, "seq_lens", dev),
+        _pool(V, f.pool, f.v_stride, "V", dev), _packed(page_table, _I32, f.table, "page_table", dev),
+        _packed(q_begin, _I32, f.begin, "q_begin", dev), _packed(seq_lens, _I32, f.seq, "seq_lens", dev),
         window, n_sinks, sm_scale, _packed(O, f.out, (n, Hq, d), "O", dev),
-        None if lse is None else _packed(lse, torch.float32, (n, Hq), "lse", dev), w, nw, _stream(stream, dev))
+        None if lse is None else _packed(lse, _F32, (n, Hq), "lse", dev), w, nw, _stream(stream, dev))
     if code:
         _check("jssa_paged_attn", code)
 
@@ -198,7 +201,7 @@ def pages_fork(L, src, dst, page_table, ref_count, seq_lens, ws, stream=None):
     dev, f = _device(), _facts(L)
     s, n = _list(src, "src", dev)
     code = load().jssa_pages_fork(
-        C.byref(L), s, _packed(dst, torch.int32, (n,), "dst", dev), n,
+        C.byref(L), s, _packed(dst, _I32, (n,), "dst", dev), n,
         *_book(f, page_table, ref_count, seq_lens, dev), *_ws(ws, dev), _stream(stream, dev))
     if code:
         _check("jssa_pages_fork", code)
@@ -209,8 +212,8 @@ def pages_reserve(L, n_new, page_table, ref_count, seq_lens, copy_src, copy_dst,
     name the shared pages to copy (pages_copy) before the append."""
     dev, f = _device(), _facts(L)
     code = load().jssa_pages_reserve(
-        C.byref(L), _packed(n_new, torch.int32, f.seq, "n_new", dev), *_book(f, page_table, ref_count, seq_lens, dev),
-        _packed(copy_src, torch.int32, f.seq, "copy_src", dev), _packed(copy_dst, torch.int32, f.seq, "copy_dst", dev),
+        C.byref(L), _packed(n_new, _I32, f.seq, "n_new", dev), *_book(f, page_table, ref_count, seq_lens, dev),
+        _packed(copy_src, _I32, f.seq, "copy_src", dev), _packed(copy_dst, _I32, f.seq, "copy_dst", dev),
         *_ws(ws, dev), _stream(stream, dev))
     if code:
         _check("jssa_pages_reserve", code)
@@ -221,7 +224,7 @@ def pages_release(L, ended, window: int, n_sinks: int, page_table, ref_count, se
     behind their last `window` tokens that hold none of the first n_sinks."""
     dev, f = _device(), _facts(L)
     code = load().jssa_pages_release(
-        C.byref(L), None if ended is None else _packed(ended, torch.int32, f.seq, "ended", dev), window, n_sinks,
+        C.byref(L), None if ended is None else _packed(ended, _I32, f.seq, "ended", dev), window, n_sinks,
         *_book(f, page_table, ref_count, seq_lens, dev), *_ws(ws, dev), _stream(stream, dev))
     if code:
         _check("jssa_pages_release", code)
@@ -233,9 +236,9 @@ def pages_compact(L, page_table, ref_count, src, dst, n_moves, ws, stream=None):
     dev, f = _device(), _facts(L)
     s, n = _list(src, "src", dev)
     code = load().jssa_pages_compact(
-        C.byref(L), _packed(page_table, torch.int32, f.table, "page_table", dev),
-        _packed(ref_count, torch.int32, f.ref, "ref_count", dev), s, _packed(dst, torch.int32, (n,), "dst", dev), n,
-        _packed(n_moves, torch.int32, (1,), "n_moves", dev), *_ws(ws, dev), _stream(stream, dev))
+        C.byref(L), _packed(page_table, _I32, f.table, "page_table", dev),
+        _packed(ref_count, _I32, f.ref, "ref_count", dev), s, _packed(dst, _I32, (n,), "dst", dev), n,
+        _packed(n_moves, _I32, (1,), "n_moves", dev), *_ws(ws, dev), _stream(stream, dev))
     if code:
         _check("jssa_pages_compact", code)
 
@@ -247,8 +250,8 @@ def pages_copy(L, K, V, src, dst, count=None, ws=None, stream=None):
     s, n = _list(src, "src", dev)
     code = load().jssa_pages_copy(
         C.byref(L), _pool(K, f.pool, f.k_stride, "K", dev), _pool(V, f.pool, f.v_stride, "V", dev), s,
-        _packed(dst, torch.int32, (n,), "dst", dev), n,
-        None if count is None else _packed(count, torch.int32, (1,), "count", dev), *_ws(ws, dev),
+        _packed(dst, _I32, (n,), "dst", dev), n,
+        None if count is None else _packed(count, _I32, (1,), "count", dev), *_ws(ws, dev),
         _stream(stream, dev))
     if code:
         _check("jssa_pages_copy", code)

@@ -171,7 +171,7 @@ jssa_status jssa_paged_attn(const jssa_paged_layout* L, const void* Q, int64_t q
   if (n_tokens < 0 || n_tokens > kInt31 || max_q_len < 0 || window < 0 || n_sinks < 0 ||
       q_stride < static_cast<int64_t>(L->Hq) * L->d || q_stride % 8 || q_stride >= (int64_t(1) << 39))
     return JSSA_ERR_INVALID_ARG;
-  if (!(sm_scale > 0.f) || sm_scale > 3e38f) return JSSA_ERR_INVALID_ARG;
+  if (!(sm_scale > 0.f) || sm_scale > 2e38f) return JSSA_ERR_INVALID_ARG;  // its product with log2 e stays finite
   if (n_tokens == 0 || max_q_len == 0) return JSSA_OK;
   if (!rows16({Q, K, V, O}) || !ints({page_table, q_begin, seq_lens}) || (lse && !aligned(lse, 4)))
     return JSSA_ERR_INVALID_ARG;

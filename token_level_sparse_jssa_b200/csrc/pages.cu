@@ -98,13 +98,14 @@ __global__ void __launch_bounds__(256) pages_fork_kernel(PageBook k, const int32
 // and m growers is given up by every grower but, when m = r, the last one (sequence by
 // sequence, each that leaves lowers the count, and the last finds itself alone): m and the
 // highest grower come from two atomics per page in `growers`, cleared again before the end.
-// The free pages are listed in ascending order, 16 counts per thread and pass, until enough
-// are found; then a warp per sequence writes the entries.
-constexpr int kReservePer = 16;
+// The free pages are listed in ascending order until enough are found: a pass takes 16 x 1024
+// counts, a ballot per 32 of them, and one scan over the 512 ballots ranks them all.  The first
+// 4096 stay in shared memory.  Then a warp per sequence writes the entries.
+constexpr int kReservePer = 16, kReserveNear = 4096;
 __global__ void __launch_bounds__(1024) pages_reserve_kernel(PageBook k, const int32_t* n_new, int32_t* copy_src,
                                                              int32_t* copy_dst, int32_t* growers, int32_t* free_list) {
   __shared__ int part[33];
-  __shared__ int lo_s[1024], cnt_s[1024], off_s[1024];
+  __shared__ int lo_s[1024], cnt_s[1024], off_s[1024], votes_s[kReservePer * 32], near_s[kReserveNear];
   const int b = threadIdx.x;
   const int ps = k.page_size;
   int len = 0, add = 0, last = -1;
@@ -157,21 +158,38 @@ __global__ void __launch_bounds__(1024) pages_reserve_kernel(PageBook k, const i
   cnt_s[b] = cnt;
   off_s[b] = off;
   int found = 0;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int64_t base = 0; !fail && base < k.n_pages && found < total; base += 1024 * kReservePer) {
-    const int64_t p0 = base + static_cast<int64_t>(threadIdx.x) * kReservePer;
-    uint32_t free_bits = 0;
+    uint32_t votes[kReservePer];
+    int ref[kReservePer];
 #pragma unroll
-    for (int u = 0; u < kReservePer; ++u)
-      if (p0 + u < k.n_pages && __ldcg(k.ref + p0 + u) <= 0) free_bits |= 1u << u;
+    for (int u = 0; u < kReservePer; ++u) {
+      const int64_t page = base + u * 1024 + threadIdx.x;
+      ref[u] = page < k.n_pages ? __ldcg(k.ref + page) : 1;
+    }
+#pragma unroll
+    for (int u = 0; u < kReservePer; ++u) {
+      votes[u] = __ballot_sync(0xFFFFFFFFu, ref[u] <= 0);
+      if (lane == 0) votes_s[u * 32 + warp] = __popc(votes[u]);
+    }
+    __syncthreads();
     int here;
-    int rank = found + block_exclusive_scan(__popc(free_bits), part, &here);
-    while (free_bits && rank < total) {
-      const int u = __ffs(free_bits) - 1;
-      free_bits &= free_bits - 1;
-      free_list[rank++] = static_cast<int>(p0) + u;
+    const int at = found + block_exclusive_scan(threadIdx.x < kReservePer * 32 ? votes_s[threadIdx.x] : 0, part, &here);
+    if (threadIdx.x < kReservePer * 32) votes_s[threadIdx.x] = at;
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kReservePer; ++u) {
+      const int rank = votes_s[u * 32 + warp] + __popc(votes[u] & ((1u << lane) - 1u));
+      if (((votes[u] >> lane) & 1) && rank < total) {
+        const int page = static_cast<int>(base) + u * 1024 + static_cast<int>(threadIdx.x);
+        if (rank < kReserveNear) near_s[rank] = page;
+        else free_list[rank] = page;
+      }
     }
     found += here;
+    __syncthreads();
   }
+  auto nth_free = [&](int rank) { return rank < kReserveNear ? near_s[rank] : __ldcg(free_list + rank); };
   if (found < total) fail = true;
   if (fail) {
     if (b < k.B) copy_src[b] = copy_dst[b] = -1;
@@ -180,17 +198,17 @@ __global__ void __launch_bounds__(1024) pages_reserve_kernel(PageBook k, const i
   }
   __threadfence_block();
   __syncthreads();
-  for (int q = threadIdx.x >> 5; q < k.B; q += 32) {
+  for (int q = warp; q < k.B; q += 32) {
     int32_t* row = k.table + static_cast<int64_t>(q) * k.max_pages + lo_s[q];
-    for (int j = threadIdx.x & 31; j < cnt_s[q]; j += 32) {
-      const int p = __ldcg(free_list + off_s[q] + j);
+    for (int j = lane; j < cnt_s[q]; j += 32) {
+      const int p = nth_free(off_s[q] + j);
       row[j] = p;
       k.ref[p] = 1;
     }
   }
   if (b < k.B) {
     copy_src[b] = split ? last : -1;
-    copy_dst[b] = split ? __ldcg(free_list + off) : -1;
+    copy_dst[b] = split ? nth_free(off) : -1;
     if (split) atomicSub(k.ref + last, 1);
     if (add > 0) k.seq_lens[b] = len + add;
   }
@@ -231,10 +249,24 @@ __global__ void __launch_bounds__(256) pages_release_kernel(PageBook k, const in
 // One cluster of 8 blocks; block c takes a contiguous slice of the pages.  Pass 1 counts the
 // pages in use: m = their number.  Pass 2 counts those below m; the holes below m and the
 // pages in use at or above m are equally many.  Pass 3 ranks and lists both.  Then the counts
-// move, and a second kernel rewrites the table through map[page] = rank of its move.
+// move, and the table is rewritten through map[page] = rank of its move: by the same launch
+// where the table has few entries, by a second one over the whole GPU otherwise.
 constexpr int kCompactBlocks = 8;
+constexpr int64_t kCompactEntries = 1 << 16;  // 8 passes of the cluster's threads
+__device__ __forceinline__ void remap_entries(const PageBook& k, const int32_t* dst, const int32_t* map, int m, int64_t i0,
+                                              int64_t step) {
+  const int64_t n = static_cast<int64_t>(k.B) * k.max_pages;
+  for (int64_t i = i0; i < n; i += step) {
+    const int p = k.table[i];
+    if (p >= m && p < k.n_pages) {
+      const int r = __ldcg(map + p);
+      if (r >= 0) k.table[i] = __ldcg(dst + r);
+    }
+  }
+}
 __global__ void __launch_bounds__(1024) __cluster_dims__(kCompactBlocks, 1, 1)
-    pages_compact_kernel(PageBook k, int32_t* src, int32_t* dst, int max_moves, int32_t* n_moves, int32_t* map) {
+    pages_compact_kernel(PageBook k, int32_t* src, int32_t* dst, int max_moves, int32_t* n_moves, int32_t* map,
+                         bool remap) {
   __shared__ int part[33];
   __shared__ int live_s, low_s;
   cg::cluster_group cluster = cg::this_cluster();
@@ -289,19 +321,12 @@ __global__ void __launch_bounds__(1024) __cluster_dims__(kCompactBlocks, 1, 1)
     k.ref[t] = k.ref[s];
     k.ref[s] = 0;
   }
+  if (remap) remap_entries(k, dst, map, m, c * 1024 + static_cast<int>(threadIdx.x), kCompactBlocks * 1024);
 }
 
 __global__ void __launch_bounds__(256) pages_remap_kernel(PageBook k, const int32_t* dst, const int32_t* map) {
-  const int m = map[k.n_pages];
-  const int64_t n = static_cast<int64_t>(k.B) * k.max_pages;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
-       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const int p = k.table[i];
-    if (p >= m && p < k.n_pages) {
-      const int r = map[p];
-      if (r >= 0) k.table[i] = dst[r];
-    }
-  }
+  remap_entries(k, dst, map, map[k.n_pages], static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x,
+                static_cast<int64_t>(gridDim.x) * blockDim.x);
 }
 
 // ------------------------------------------------------------------ copy and append
@@ -422,10 +447,12 @@ cudaError_t launch_pages_release(const PageBook& k, const int32_t* ended, int wi
 
 cudaError_t launch_pages_compact(const PageBook& k, int32_t* src, int32_t* dst, int max_moves, int32_t* n_moves,
                                  int32_t* map, cudaStream_t s) {
+  const int64_t entries = static_cast<int64_t>(k.B) * k.max_pages;
+  const bool remap = entries <= kCompactEntries;
   cudaError_t e = launch_ex(pages_compact_kernel, dim3(kCompactBlocks), dim3(1024), 0, s, 0, k, src, dst, max_moves,
-                            n_moves, map);
-  if (e != cudaSuccess) return e;
-  const int64_t blocks = ceil_div(static_cast<int64_t>(k.B) * k.max_pages, 256);
+                            n_moves, map, remap);
+  if (e != cudaSuccess || remap) return e;
+  const int64_t blocks = ceil_div(entries, 256);
   return launch_ex(pages_remap_kernel, dim3(static_cast<unsigned>(min64(blocks, 1024))), dim3(256), 0, s, 0, k,
                    static_cast<const int32_t*>(dst), static_cast<const int32_t*>(map));
 }
