@@ -110,6 +110,13 @@ __device__ __forceinline__ Item item_at(const PaParams& p, int nq, int len, int 
   return it;
 }
 
+// Items of more than a warp's rows, each row whole in one accumulator, are merged by a thread per row; the
+// others word by word.
+template <int D>
+__device__ __forceinline__ bool tall_item(const Item& it, int G) {
+  return (!it.solo || Pa<D>::kWG == 1) && it.ntok * G > 32;
+}
+
 // An item's length on the line: a tile of two query tiles counts twice, and what a piece costs
 // before its first tile and after its last stands at the front.
 constexpr int kPaItemUnits = 8;
@@ -423,8 +430,13 @@ __device__ __forceinline__ void merge_pieces(const PaParams& p, const Piece& s) 
   const int words = s.it.ntok * p.G * (D / 4);
   int sh = 0;
   while (sh < 5 && (words << (sh + 1)) <= Pa<D>::kSoftmax) ++sh;
-  if (words > Pa<D>::kSoftmax) merge_words<D, F32, 4, 2>(p, s, words, 0);
+  if (words > Pa<D>::kSoftmax && s.c_last - s.c_first < 8) merge_words<D, F32, 4, 2>(p, s, words, 0);
   else merge_words<D, F32, 1, 8>(p, s, words, sh);
+}
+
+// 16-byte word w of a two-query-tile piece's rows in the workspace: row after row.
+__device__ __forceinline__ float4* part_word(const PagedAttnArgs& a, int d, int slot, int w) {
+  return reinterpret_cast<float4*>(a.part_o) + (static_cast<int64_t>(slot) * (d / 4) + w) * a.rows_cap;
 }
 
 template <int D, bool F32>
@@ -451,6 +463,7 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
 
   // ---- each sequence's length on the line (per KV head), into the ring, which is still empty
   int64_t* seq_units = reinterpret_cast<int64_t*>(smem_raw + kWG * C::kQBytes);
+  float* seq_merge = reinterpret_cast<float*>(seq_units + 1024);
   {
     // a warp per sequence where sequences may have many items, a thread otherwise
     const int tpi = p.tpt * kWG;
@@ -460,13 +473,25 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
       const NewTokens t = new_tokens(a.q_begin, a.seq_lens, b, cap, a.n_tokens, a.max_q_len,
                                      blockIdx.x == 0 ? a.status : nullptr);
       int64_t n = 0;
-      for (int j = wide ? lane : 0; j * static_cast<int64_t>(tpi) < t.nq; j += wide ? 32 : 1)
-        n += item_units(item_at<D>(p, t.nq, t.len, j));
+      float merge = 0.f;  // the largest product of an item's length and what one more piece of it costs, in units
+      for (int j = wide ? lane : 0; j * static_cast<int64_t>(tpi) < t.nq; j += wide ? 32 : 1) {
+        const Item it = item_at<D>(p, t.nq, t.len, j);
+        const int64_t u = item_units(it);
+        n += u;
+        const float cost = tall_item<D>(it, p.G) ? D / 64 : it.ntok * p.G * (D / 8192.f);
+        merge = fmaxf(merge, u * cost);
+      }
       if (wide) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
+        for (int o = 16; o > 0; o >>= 1) {
+          n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
+          merge = fmaxf(merge, __shfl_xor_sync(0xFFFFFFFFu, merge, o));
+        }
       }
-      if (!wide || lane == 0) seq_units[b] = n;
+      if (!wide || lane == 0) {
+        seq_units[b] = n;
+        seq_merge[b] = merge;
+      }
     }
   }
   if (tid == 0) {
@@ -690,7 +715,7 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
         l = f0 * l0 + f1 * l1;
       }
       tc_fence_after();
-      const bool whole = s.c_first == s.c_last;
+      const bool whole = s.c_first == s.c_last, tall = tall_item<D>(s.it, p.G);
       const int row = (solo ? 0 : wg * rows_tile) + r;  // within the item
       const int64_t orow = (s.q0 + row / p.G) * a.Hq + s.h * p.G + row % p.G;
       const int slot_out = 2 * static_cast<int>(blockIdx.x) + (static_cast<int>(blockIdx.x) == s.c_first ? 1 : 0);
@@ -714,7 +739,13 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
 #pragma unroll
             for (int e = 0; e < 32; ++e) v[e] *= g;
             if (whole) store_out32<F32>(a.O, orow * D + 32 * c, v);
-            else store_out32<true>(a.part_o, prow * D + 32 * c, v);
+            else if (!tall) store_out32<true>(a.part_o, prow * D + 32 * c, v);
+            else {  // word by word, the rows side by side
+              float4* to = part_word(a, D, slot_out, 8 * c) + row;
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                to[static_cast<int64_t>(e) * a.rows_cap] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+            }
           }
           __syncwarp();
         }
@@ -743,7 +774,54 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
       }
       ok = sync_wgs();
       if (!ok) break;
-      if (last_s) merge_pieces<D, F32>(p, s);
+      if (last_s && !tall) merge_pieces<D, F32>(p, s);
+      if (last_s && tall && active) {
+        // a thread per row and stream: two pieces' 32 columns under way at once
+        const int n = s.c_last - s.c_first + 1;
+        auto slot_of = [&](int k) { return 2 * (s.c_first + k) + (k == 0 ? 1 : 0); };
+        auto ml_of = [&](int k) { return __ldcg(a.part_ml + static_cast<int64_t>(slot_of(k)) * a.rows_cap + row); };
+        float M = -INFINITY, L = 0.f, z = 0.f, g = 0.f;
+        if (valid) {
+#pragma unroll 2
+          for (int k = 0; k < n; ++k) M = fmaxf(M, ml_of(k).x);
+          z = M == -INFINITY ? 0.f : M * p.scale_log2;
+#pragma unroll 2
+          for (int k = 0; k < n; ++k) {
+            const float2 ml = ml_of(k);
+            L = fmaf(exp2_approx(fmaf(ml.x, p.scale_log2, -z)), ml.y, L);
+          }
+          g = L > 0.f ? 1.f / L : 0.f;
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            float acc[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) acc[e] = 0.f;
+#pragma unroll 1
+            for (int k = 0; k < n; k += 2) {
+              const int k2 = min(k + 1, n - 1);
+              const float4* f0 = part_word(a, D, slot_of(k), 8 * c) + row;
+              const float4* f1 = part_word(a, D, slot_of(k2), 8 * c) + row;
+              float4 y0[8], y1[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                y0[e] = __ldcg(f0 + static_cast<int64_t>(e) * a.rows_cap);
+                y1[e] = __ldcg(f1 + static_cast<int64_t>(e) * a.rows_cap);
+              }
+              const float w0 = exp2_approx(fmaf(ml_of(k).x, p.scale_log2, -z)) * g;
+              const float w1 = k2 > k ? exp2_approx(fmaf(ml_of(k2).x, p.scale_log2, -z)) * g : 0.f;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                acc[4 * e] = fmaf(w1, y1[e].x, fmaf(w0, y0[e].x, acc[4 * e]));
+                acc[4 * e + 1] = fmaf(w1, y1[e].y, fmaf(w0, y0[e].y, acc[4 * e + 1]));
+                acc[4 * e + 2] = fmaf(w1, y1[e].z, fmaf(w0, y0[e].z, acc[4 * e + 2]));
+                acc[4 * e + 3] = fmaf(w1, y1[e].w, fmaf(w0, y0[e].w, acc[4 * e + 3]));
+              }
+            }
+            store_out32<F32>(a.O, orow * D + 32 * c, acc);
+          }
+        }
+        if (valid && a.lse) a.lse[orow] = L > 0.f ? M * a.sm_scale + logf(L) : -INFINITY;
+      }
       release(piece);
     }
   } else {
@@ -757,7 +835,11 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
       // the line's length, and the item that this CTA's stretch of it begins in
       const int per = (a.B + 31) / 32;
       int64_t mine = 0;
-      for (int e = 0; e < per && lane * per + e < a.B; ++e) mine += seq_units[lane * per + e] * a.pool.Hkv;
+      float merge = 0.f;
+      for (int e = 0; e < per && lane * per + e < a.B; ++e) {
+        mine += seq_units[lane * per + e] * a.pool.Hkv;
+        merge = fmaxf(merge, seq_merge[lane * per + e]);
+      }
       int64_t before = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -766,8 +848,12 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
       }
       const int64_t total = __shfl_sync(0xFFFFFFFFu, before, 31);
       before -= mine;
-      // at least two units per CTA, so that each cut piece has a whole tile
-      const int nact = static_cast<int>(min64(gridDim.x, max64(1, total / 2)));
+      // A CTA has two units at least, so that each cut piece has a whole tile, and no less than balances an
+      // item's time in pieces of u units, u, against the time to merge them, cost * length / u.
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) merge = fmaxf(merge, __shfl_xor_sync(0xFFFFFFFFu, merge, o));
+      const int64_t least = max64(2, static_cast<int64_t>(sqrtf(merge)));
+      const int nact = static_cast<int>(min64(gridDim.x, max64(1, quotient(total, least))));
       const Cuts cuts(total, nact);
       const bool idle = total == 0 || static_cast<int>(blockIdx.x) >= nact;
       int64_t at = 0;
