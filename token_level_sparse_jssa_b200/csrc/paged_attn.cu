@@ -38,7 +38,7 @@
 
 #include "common.cuh"
 #include "launch.h"
-#include "paged.cuh"
+#include "paged_line.cuh"
 #include "tcgen05.cuh"
 
 namespace jssa {
@@ -48,12 +48,11 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kPaOCol = 256;   // first TMEM column of O; S (and P over it) below
 constexpr float kPaRescale = 8.f;   // log2 margin before the running maximum moves
 constexpr int kPaCubicEvery = 8;    // of so many pairs of exponentials, one goes to the FMA pipe
-constexpr int kPaPieces = 4;        // pieces published at once
-constexpr int kPaBadRing = 16;      // tiles whose missing pages are remembered
-constexpr float kLog2e = 1.4426950408889634f;
 
 template <int D>
 struct Pa {
+  static constexpr int kD = D;
+  static constexpr int kItemUnits = 8;
   static constexpr int kTile = D == 256 ? 64 : 128;      // keys per tile
   static constexpr int kWG = D == 256 ? 1 : 2;           // softmax warpgroups
   static constexpr int kDB = D / 64;                     // 64-dim blocks of a row
@@ -67,184 +66,6 @@ struct Pa {
   static constexpr int kThreads = kSoftmax + 128;
   static constexpr uint32_t kSCols = kTile;              // columns of one S slot (two slots)
 };
-
-struct PaParams {
-  CUtensorMap q, k, v;
-  PagedAttnArgs a;
-  int G, tpt;      // query heads per KV head; tokens per query tile
-  int box, nbox;   // rows of a TMA box (a power of two); boxes per tile
-  int tile_pages, tile_rows;  // a tile's length in pages and rows
-  float scale_log2;
-};
-
-// One item: its tokens and the list of its keys.  Place v of the list holds token v below s_al
-// and token v + shift from there on; z0 <= v < z1 and v >= nv are seen by no query.
-struct Item {
-  int tok0, ntok, pf;
-  int s_al, shift, z0, z1, nv, ntiles;
-  bool solo;  // one query tile
-};
-
-template <int D>
-__device__ __forceinline__ Item item_at(const PaParams& p, int nq, int len, int j) {
-  Item it;
-  const int tpi = p.tpt * Pa<D>::kWG;
-  it.tok0 = j * tpi;
-  it.ntok = min(tpi, nq - it.tok0);
-  it.pf = len - nq + it.tok0;
-  const int hi = it.pf + it.ntok;
-  it.s_al = it.shift = it.z0 = it.z1 = 0;
-  if (p.a.window > 0) {
-    const int lo = max(0, it.pf + 1 - p.a.window), lo_al = lo & ~(p.box - 1);
-    it.z0 = min(p.a.n_sinks, lo);
-    const int s_al = (it.z0 + p.box - 1) & ~(p.box - 1);
-    if (s_al < lo_al) {
-      it.s_al = s_al;
-      it.shift = lo_al - s_al;
-    }
-    it.z1 = lo - it.shift;
-  }
-  it.nv = hi - it.shift;
-  it.ntiles = (it.nv + Pa<D>::kTile - 1) / Pa<D>::kTile;
-  it.solo = Pa<D>::kWG == 1 || it.ntok <= p.tpt;
-  return it;
-}
-
-// Items of more than a warp's rows, each row whole in one accumulator, are merged by a thread per row; the
-// others word by word.
-template <int D>
-__device__ __forceinline__ bool tall_item(const Item& it, int G) {
-  return (!it.solo || Pa<D>::kWG == 1) && it.ntok * G > 32;
-}
-
-// An item's length on the line: a tile of two query tiles counts twice, and what a piece costs
-// before its first tile and after its last stands at the front.
-constexpr int kPaItemUnits = 8;
-__device__ __forceinline__ int64_t item_units(const Item& it) {
-  return kPaItemUnits + (it.solo ? it.ntiles : 2 * static_cast<int64_t>(it.ntiles));
-}
-
-// Quotient of non-negative numbers, on the 32-bit path where both fit.
-__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
-  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-  return a / b;
-}
-
-// The cuts of the line: CTA c has [start(c), start(c + 1)).
-struct Cuts {
-  int64_t len, more;  // `more` CTAs have len + 1 units
-  __device__ Cuts(int64_t total, int n) : len(quotient(total, n)), more(total - len * n) {}
-  __device__ int64_t start(int c) const { return c * len + min64(c, more); }
-  __device__ int owner(int64_t x) const {  // of place x
-    const int64_t y = x - more * (len + 1);
-    return static_cast<int>(y < 0 ? quotient(x, len + 1) : more + quotient(y, len));
-  }
-};
-
-// A CTA's share of one item: tiles [t0, t1); t1 = 0 ends the CTA's work.  CTAs c_first to c_last share the item.
-struct Piece {
-  Item it;
-  int64_t q0;  // first token's row
-  int b, h, t0, t1, c_first, c_last;
-};
-
-// Walks the pieces that fall to this CTA, in order.
-template <int D>
-struct Walk {
-  const PaParams& p;
-  Cuts cuts;
-  int64_t u, u0, u1, q0;
-  int b, h, j, nq, len;
-
-  __device__ Walk(const PaParams& pp, const Cuts& cc, int64_t start, int b0, int h0, int j0)
-      : p(pp), cuts(cc), u(start), b(b0), h(h0), j(j0) {
-    u0 = cuts.start(blockIdx.x);
-    u1 = cuts.start(blockIdx.x + 1);
-    load();
-  }
-  __device__ void load() {
-    const NewTokens t = new_tokens(p.a.q_begin, p.a.seq_lens, b,
-                                   static_cast<int64_t>(p.a.max_pages) * p.a.pool.page_size, p.a.n_tokens,
-                                   p.a.max_q_len, nullptr);
-    q0 = t.q0, nq = t.nq, len = t.len;
-  }
-  __device__ Piece next() {
-    Piece c;
-    c.t1 = 0;
-    while (u < u1) {
-      c.it = item_at<D>(p, nq, len, j);
-      const int w = c.it.solo ? 1 : 2;
-      const int64_t at = u + kPaItemUnits;  // tile i belongs to the CTA that has place at + w i
-      c.t0 = at >= u0 ? 0 : static_cast<int>((u0 - at + w - 1) / w);
-      c.t1 = at >= u1 ? 0 : static_cast<int>(min64(c.it.ntiles, (u1 - at + w - 1) / w));
-      c.b = b, c.h = h, c.q0 = q0 + c.it.tok0;
-      u += item_units(c.it);
-      ++j;
-      if (c.it.tok0 + c.it.ntok == nq) {
-        j = 0;
-        if (++h == p.a.pool.Hkv) {
-          h = 0;
-          do {
-            if (++b == p.a.B) break;
-            load();
-          } while (nq == 0);
-        }
-      }
-      if (c.t0 < c.t1) {
-        c.c_first = at >= u0 ? static_cast<int>(blockIdx.x) : cuts.owner(at);
-        c.c_last = c.t1 == c.it.ntiles ? static_cast<int>(blockIdx.x)
-                                       : cuts.owner(at + static_cast<int64_t>(w) * (c.it.ntiles - 1));
-        return c;
-      }
-      c.t1 = 0;
-    }
-    return c;
-  }
-};
-
-struct Waiter {
-  volatile int* dead;
-  int* status;
-  // The hint lets a waiting warp sleep in the barrier unit; the clock is read every 64 wake-ups, because
-  // waiting warps share the issue slots with the ones at work.
-  __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
-    uint64_t t0 = 0;
-    for (uint32_t n = 0;; ++n) {
-      uint32_t done;
-      asm volatile(
-          "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
-          " selp.u32 %0, 1, 0, p;\n}\n"
-          : "=r"(done)
-          : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
-          : "memory");
-      if (done) return true;
-      if (*dead) return false;
-      if (n % 64 == 63) {
-        const uint64_t t = global_timer_ns();
-        if (t0 == 0) t0 = t;
-        if (t - t0 > kWaitLimitNs) {
-          flag_error(status, DEVFLAG_TIMEOUT);
-          *dead = 1;
-          return false;
-        }
-      }
-    }
-  }
-};
-
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-
-__device__ __forceinline__ void prefetch_tensormap(const void* map) {
-  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
-}
-
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 // Two fp32 values in one 64-bit register, and the packed arithmetic on them.
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
@@ -286,159 +107,6 @@ __device__ __forceinline__ uint64_t exp2_cubic2(uint64_t x) {
                __uint_as_float(__float_as_uint(b) + (__float_as_uint(nb) << 23)));
 }
 
-// Bits [0, n) of a word, n clamped to [0, 32].
-__device__ __forceinline__ uint32_t bits_below(int n) { return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u); }
-
-// One box of an item's tiles, from tile to tile: its page-table entry and row within the page.
-template <int D>
-struct BoxWalk {
-  int v, slot, row;
-  __device__ void place(const PaParams& p, const Item& it) {
-    const int t = v < it.s_al ? v : v + it.shift;
-    slot = t / p.a.pool.page_size;
-    row = t - slot * p.a.pool.page_size;
-  }
-  __device__ BoxWalk(const PaParams& p, const Piece& s, int box) : v(s.t0 * Pa<D>::kTile + box * p.box) {
-    place(p, s.it);
-  }
-  // Page of the box: -2 where the item has no keys, -1 where the table names no page.
-  __device__ int page(const PaParams& p, const Piece& s, bool on) const {
-    if (!on || v >= s.it.nv) return -2;
-    const int pg = __ldg(p.a.table + static_cast<int64_t>(s.b) * p.a.max_pages + slot);
-    return pg < 0 || pg >= p.a.pool.n_pages ? -1 : pg;
-  }
-  __device__ void step(const PaParams& p, const Item& it) {
-    const bool sink = v < it.s_al;
-    v += Pa<D>::kTile;
-    if (sink && v >= it.s_al) {
-      place(p, it);
-    } else {
-      slot += p.tile_pages;
-      row += p.tile_rows;
-      if (row >= p.a.pool.page_size) row -= p.a.pool.page_size, ++slot;
-    }
-  }
-};
-
-// Whether tile i holds rows that no query of the item sees.
-template <int D>
-__device__ __forceinline__ bool edge_tile(const Item& it, int i) {
-  const int v0 = i * Pa<D>::kTile, v1 = v0 + Pa<D>::kTile;
-  return v1 > it.nv || (it.z0 < it.z1 && v0 < it.z1 && v1 > it.z0);
-}
-
-// Stores 32 consecutive outputs of a row.
-template <bool F32>
-__device__ __forceinline__ void store_out32(void* O, int64_t at, const float (&v)[32]) {
-  if constexpr (F32) {
-    float4* o = reinterpret_cast<float4*>(static_cast<float*>(O) + at);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-  } else {
-    uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(O) + at);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      o[i] = make_uint4(pack_bf16x2(v[8 * i], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
-                        pack_bf16x2(v[8 * i + 4], v[8 * i + 5]), pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
-  }
-}
-
-// Merges the pieces of a cut item in their order: the softmax threads of the CTA that finishes it
-// last.  A thread takes kWords 16-byte words of rows at a time and kParts partials of each at once;
-// with fewer words than threads, 2^sh neighbouring lanes share a word's partials.
-template <int D, bool F32, int kWords, int kParts>
-__device__ __forceinline__ void merge_words(const PaParams& p, const Piece& s, int words, int sh) {
-  const PagedAttnArgs& a = p.a;
-  const int n = s.c_last - s.c_first + 1, part = threadIdx.x & ((1 << sh) - 1), wstep = Pa<D>::kSoftmax >> sh;
-  for (int w0 = 0; w0 < words; w0 += kWords * wstep) {
-    float4 o[kWords];
-    float M[kWords], L[kWords];
-    int row[kWords], col[kWords];
-#pragma unroll
-    for (int x = 0; x < kWords; ++x) {
-      const int idx = w0 + x * wstep + (threadIdx.x >> sh);
-      row[x] = idx < words ? idx / (D / 4) : -1;
-      col[x] = idx % (D / 4);
-      o[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-      M[x] = -INFINITY;
-      L[x] = 0.f;
-    }
-    for (int k0 = part; k0 < n; k0 += kParts << sh) {
-      float2 ml[kWords][kParts];
-      float4 v[kWords][kParts];
-#pragma unroll
-      for (int x = 0; x < kWords; ++x)
-#pragma unroll
-        for (int y = 0; y < kParts; ++y) {
-          const int k = k0 + (y << sh);
-          ml[x][y] = make_float2(-INFINITY, 0.f);
-          v[x][y] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (row[x] < 0 || k >= n) continue;
-          // an item's first piece is the last of its CTA, the others the first of theirs
-          const int64_t at = static_cast<int64_t>(2 * (s.c_first + k) + (k == 0 ? 1 : 0)) * a.rows_cap + row[x];
-          ml[x][y] = __ldcg(&a.part_ml[at]);
-          v[x][y] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * D) + col[x]);
-        }
-#pragma unroll
-      for (int x = 0; x < kWords; ++x) {
-        float mn = M[x];
-#pragma unroll
-        for (int y = 0; y < kParts; ++y) mn = fmaxf(mn, ml[x][y].x);  // a piece without keys has m = -infinity
-        const float z = mn == -INFINITY ? 0.f : mn * p.scale_log2;
-        const float w = exp2_approx(fmaf(M[x], p.scale_log2, -z));
-        M[x] = mn;
-        L[x] *= w;
-        o[x].x *= w, o[x].y *= w, o[x].z *= w, o[x].w *= w;
-#pragma unroll
-        for (int y = 0; y < kParts; ++y) {
-          const float u = exp2_approx(fmaf(ml[x][y].x, p.scale_log2, -z));
-          L[x] = fmaf(u, ml[x][y].y, L[x]);
-          o[x].x = fmaf(u, v[x][y].x, o[x].x), o[x].y = fmaf(u, v[x][y].y, o[x].y);
-          o[x].z = fmaf(u, v[x][y].z, o[x].z), o[x].w = fmaf(u, v[x][y].w, o[x].w);
-        }
-      }
-    }
-#pragma unroll
-    for (int x = 0; x < kWords; ++x) {
-      for (int y = 1; y < 1 << sh; y <<= 1) {
-        const float m2 = __shfl_xor_sync(0xFFFFFFFFu, M[x], y), l2 = __shfl_xor_sync(0xFFFFFFFFu, L[x], y);
-        const float mn = fmaxf(M[x], m2), z = mn == -INFINITY ? 0.f : mn * p.scale_log2;
-        const float w1 = exp2_approx(fmaf(M[x], p.scale_log2, -z)), w2 = exp2_approx(fmaf(m2, p.scale_log2, -z));
-        M[x] = mn;
-        L[x] = w1 * L[x] + w2 * l2;
-        o[x].x = w1 * o[x].x + w2 * __shfl_xor_sync(0xFFFFFFFFu, o[x].x, y);
-        o[x].y = w1 * o[x].y + w2 * __shfl_xor_sync(0xFFFFFFFFu, o[x].y, y);
-        o[x].z = w1 * o[x].z + w2 * __shfl_xor_sync(0xFFFFFFFFu, o[x].z, y);
-        o[x].w = w1 * o[x].w + w2 * __shfl_xor_sync(0xFFFFFFFFu, o[x].w, y);
-      }
-      if (part != 0 || row[x] < 0) continue;
-      const float g = L[x] > 0.f ? 1.f / L[x] : 0.f;
-      o[x].x *= g, o[x].y *= g, o[x].z *= g, o[x].w *= g;
-      const int64_t to = (s.q0 + row[x] / p.G) * a.Hq + s.h * p.G + row[x] % p.G;
-      if constexpr (F32)
-        reinterpret_cast<float4*>(static_cast<float*>(a.O) + to * D)[col[x]] = o[x];
-      else
-        reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.O) + to * D)[col[x]] =
-            make_uint2(pack_bf16x2(o[x].x, o[x].y), pack_bf16x2(o[x].z, o[x].w));
-      if (col[x] == 0 && a.lse) a.lse[to] = L[x] > 0.f ? M[x] * a.sm_scale + logf(L[x]) : -INFINITY;
-    }
-  }
-}
-
-template <int D, bool F32>
-__device__ __forceinline__ void merge_pieces(const PaParams& p, const Piece& s) {
-  const int words = s.it.ntok * p.G * (D / 4);
-  int sh = 0;
-  while (sh < 5 && (words << (sh + 1)) <= Pa<D>::kSoftmax) ++sh;
-  if (words > Pa<D>::kSoftmax && s.c_last - s.c_first < 8) merge_words<D, F32, 4, 2>(p, s, words, 0);
-  else merge_words<D, F32, 1, 8>(p, s, words, sh);
-}
-
-// 16-byte word w of a two-query-tile piece's rows in the workspace: row after row.
-__device__ __forceinline__ float4* part_word(const PagedAttnArgs& a, int d, int slot, int w) {
-  return reinterpret_cast<float4*>(a.part_o) + (static_cast<int64_t>(slot) * (d / 4) + w) * a.rows_cap;
-}
-
 template <int D, bool F32>
 __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __grid_constant__ PaParams p) {
   using C = Pa<D>;
@@ -453,7 +121,6 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const PagedAttnArgs& a = p.a;
-  const int64_t cap = static_cast<int64_t>(a.max_pages) * a.pool.page_size;
 
   if (tid == 0) {
     prefetch_tensormap(&p.q);
@@ -463,37 +130,7 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
 
   // ---- each sequence's length on the line (per KV head), into the ring, which is still empty
   int64_t* seq_units = reinterpret_cast<int64_t*>(smem_raw + kWG * C::kQBytes);
-  float* seq_merge = reinterpret_cast<float*>(seq_units + 1024);
-  {
-    // a warp per sequence where sequences may have many items, a thread otherwise
-    const int tpi = p.tpt * kWG;
-    const bool wide = a.max_q_len > 8 * tpi;
-    const int step = wide ? C::kThreads / 32 : C::kThreads;
-    for (int b = wide ? warp : tid; b < a.B; b += step) {
-      const NewTokens t = new_tokens(a.q_begin, a.seq_lens, b, cap, a.n_tokens, a.max_q_len,
-                                     blockIdx.x == 0 ? a.status : nullptr);
-      int64_t n = 0;
-      float merge = 0.f;  // the largest product of an item's length and what one more piece of it costs, in units
-      for (int j = wide ? lane : 0; j * static_cast<int64_t>(tpi) < t.nq; j += wide ? 32 : 1) {
-        const Item it = item_at<D>(p, t.nq, t.len, j);
-        const int64_t u = item_units(it);
-        n += u;
-        const float cost = tall_item<D>(it, p.G) ? D / 64 : it.ntok * p.G * (D / 8192.f);
-        merge = fmaxf(merge, u * cost);
-      }
-      if (wide) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-          n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
-          merge = fmaxf(merge, __shfl_xor_sync(0xFFFFFFFFu, merge, o));
-        }
-      }
-      if (!wide || lane == 0) {
-        seq_units[b] = n;
-        seq_merge[b] = merge;
-      }
-    }
-  }
+  line_lengths<C>(p, seq_units);
   if (tid == 0) {
     dead_s = 0;
     mbar_init(&q_full, 1);
@@ -715,7 +352,7 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
         l = f0 * l0 + f1 * l1;
       }
       tc_fence_after();
-      const bool whole = s.c_first == s.c_last, tall = tall_item<D>(s.it, p.G);
+      const bool whole = s.c_first == s.c_last, tall = tall_item<C>(s.it, p.G);
       const int row = (solo ? 0 : wg * rows_tile) + r;  // within the item
       const int64_t orow = (s.q0 + row / p.G) * a.Hq + s.h * p.G + row % p.G;
       const int slot_out = 2 * static_cast<int>(blockIdx.x) + (static_cast<int>(blockIdx.x) == s.c_first ? 1 : 0);
@@ -774,7 +411,7 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
       }
       ok = sync_wgs();
       if (!ok) break;
-      if (last_s && !tall) merge_pieces<D, F32>(p, s);
+      if (last_s && !tall) merge_pieces<C, F32>(p, s);
       if (last_s && tall && active) {
         // a thread per row and stream: two pieces' 32 columns under way at once
         const int n = s.c_last - s.c_first + 1;
@@ -832,72 +469,10 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
       const bool on = box < p.nbox;
       uint32_t st = 0, st_par = 1, used = 0, tiles = 0;  // the next stage, its phase before, stages in use; tiles begun
       bool ok = true;
-      // the line's length, and the item that this CTA's stretch of it begins in
-      const int per = (a.B + 31) / 32;
-      int64_t mine = 0;
-      float merge = 0.f;
-      for (int e = 0; e < per && lane * per + e < a.B; ++e) {
-        mine += seq_units[lane * per + e] * a.pool.Hkv;
-        merge = fmaxf(merge, seq_merge[lane * per + e]);
-      }
-      int64_t before = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xFFFFFFFFu, before, o);
-        if (lane >= o) before += v;
-      }
-      const int64_t total = __shfl_sync(0xFFFFFFFFu, before, 31);
-      before -= mine;
-      // A CTA has two units at least, so that each cut piece has a whole tile, and no less than balances an
-      // item's time in pieces of u units, u, against the time to merge them, cost * length / u.
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) merge = fmaxf(merge, __shfl_xor_sync(0xFFFFFFFFu, merge, o));
-      const int64_t least = max64(2, static_cast<int64_t>(sqrtf(merge)));
-      const int nact = static_cast<int>(min64(gridDim.x, max64(1, quotient(total, least))));
-      const Cuts cuts(total, nact);
-      const bool idle = total == 0 || static_cast<int>(blockIdx.x) >= nact;
-      int64_t at = 0;
-      int b0 = 0, h0 = 0, j0 = 0;
-      if (!idle) {
-        const int64_t u0 = cuts.start(blockIdx.x);
-        const uint32_t owner = __ballot_sync(0xFFFFFFFFu, u0 >= before && u0 < before + mine);
-        const int from = __ffs(owner) - 1;
-        at = before;
-        b0 = lane * per;
-        if (lane == from)
-          while (u0 >= at + seq_units[b0] * a.pool.Hkv) at += seq_units[b0++] * a.pool.Hkv;
-        at = __shfl_sync(0xFFFFFFFFu, at, from);
-        b0 = __shfl_sync(0xFFFFFFFFu, b0, from);
-        const int64_t per_head = seq_units[b0];
-        h0 = static_cast<int>(quotient(u0 - at, per_head));
-        at += h0 * per_head;
-        int64_t rem = u0 - at;
-        const NewTokens t = new_tokens(a.q_begin, a.seq_lens, b0, cap, a.n_tokens, a.max_q_len, nullptr);
-        for (;; j0 += 32) {
-          const int64_t tok = (j0 + lane) * static_cast<int64_t>(p.tpt * kWG);
-          const int64_t n = tok < t.nq ? item_units(item_at<D>(p, t.nq, t.len, j0 + lane)) : 0;
-          int64_t sum = n;
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const int64_t v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
-            if (lane >= o) sum += v;
-          }
-          const uint32_t past = __ballot_sync(0xFFFFFFFFu, sum > rem);
-          if (past) {
-            const int l0 = __ffs(past) - 1;
-            j0 += l0;
-            at += __shfl_sync(0xFFFFFFFFu, sum - n, l0);
-            break;
-          }
-          const int64_t all = __shfl_sync(0xFFFFFFFFu, sum, 31);
-          rem -= all;
-          at += all;
-        }
-      }
+      const Start at0 = line_start<C>(p, seq_units);
       __syncwarp();  // seq_units has been read; loads write there next
       fence_async_smem();
-      Walk<D> walk(p, cuts, at, b0, h0, j0);
-      if (idle) walk.u = walk.u1 = 0;
+      Walk<C> walk(p, at0);
       // The rest of an item that an earlier CTA began comes last: the CTAs of a head then go through its
       // keys side by side, and find them in L2.
       bool late = false;
@@ -925,7 +500,7 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
         }
         const Piece& s = pieces[at];
         if (s.t1 == 0) break;
-        BoxWalk<D> bw(p, s, box);
+        BoxWalk<C> bw(p, s, box);
         int pg_next = bw.page(p, s, on);
         if (piece > 0) ok = all_ok(wait(&q_empty, (piece - 1) & 1));
         if (!ok) break;
@@ -968,7 +543,7 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
       for (int piece = 0; ok; ++piece) {
         const Piece& s = take(piece, &ok);
         if (!ok) break;
-        BoxWalk<D> bw(p, s, box);
+        BoxWalk<C> bw(p, s, box);
         int pg_next = bw.page(p, s, on);
         for (int i = s.t0; i < s.t1; ++i) {
           const int pg = pg_next, row = bw.row;
@@ -978,7 +553,7 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
           if (!ok) break;
           const uint32_t bad = __ballot_sync(0xFFFFFFFFu, pg == -1);
           const uint32_t loads = __popc(__ballot_sync(0xFFFFFFFFu, pg >= 0));
-          uint64_t* bar = bad || edge_tile<D>(s.it, i) ? &edge_full[st] : &kv_full[st];
+          uint64_t* bar = bad || edge_tile<C>(s.it, i) ? &edge_full[st] : &kv_full[st];
           if (lane == 0) mbar_arrive_expect_tx(bar, loads * p.box * (kDB * 128));
           __syncwarp();
           if (pg >= 0)
@@ -998,7 +573,7 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
       for (int piece = 0; ok; ++piece) {
         const Piece& s = take(piece, &ok);
         if (!ok) break;
-        BoxWalk<D> bw(p, s, lane);
+        BoxWalk<C> bw(p, s, lane);
         int pg_next = bw.page(p, s, on);
         for (int i = s.t0; i < s.t1; ++i) {
           const uint32_t bad = __ballot_sync(0xFFFFFFFFu, pg_next == -1), here = st;
@@ -1006,7 +581,7 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
           pg_next = i + 1 < s.t1 ? bw.page(p, s, on) : -2;
           st += 2;
           if (st >= kNS) st -= kNS;
-          if (!bad && !edge_tile<D>(s.it, i)) continue;
+          if (!bad && !edge_tile<C>(s.it, i)) continue;
           ok = all_ok(wait(&edge_full[here], (par >> here) & 1));
           if (!ok) break;
           par ^= 1u << here;
@@ -1174,63 +749,11 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
 }
 
 // ------------------------------------------------------------------ host
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encode_tiled() {
-  static EncodeTiled fn = [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult r;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
-        r != cudaDriverEntryPointSuccess)
-      return static_cast<EncodeTiled>(nullptr);
-    return reinterpret_cast<EncodeTiled>(f);
-  }();
-  return fn;
-}
-
-// Map of a bf16 tensor whose innermost extent is d (boxes of 64 of them, 128-byte swizzle).  The
-// stride of an extent of 1 is never used and set to a row's, which the encoder accepts.
-bool encode(CUtensorMap* m, const void* base, int rank, const int64_t* extent, const int64_t* stride, const int* box) {
-  cuuint64_t dims[5], strides[4];
-  cuuint32_t boxes[5], ones[5] = {1, 1, 1, 1, 1};
-  for (int i = 0; i < rank; ++i) {
-    dims[i] = static_cast<cuuint64_t>(extent[i]);
-    boxes[i] = static_cast<cuuint32_t>(box[i]);
-    if (i > 0) strides[i - 1] = static_cast<cuuint64_t>(extent[i] > 1 ? stride[i] : extent[0]) * 2;
-  }
-  const EncodeTiled fn = encode_tiled();
-  return fn && fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank), const_cast<void*>(base), dims,
-                  strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int D, bool F32>
 cudaError_t launch(const PagedAttnArgs& a, int num_sms, cudaStream_t s) {
   using C = Pa<D>;
   PaParams p;
-  p.a = a;
-  p.G = a.Hq / a.pool.Hkv;
-  p.tpt = paged_attn_tile_tokens(p.G);
-  p.box = 16;  // the largest power of two that divides a page, at most a tile
-  while (p.box < C::kTile && a.pool.page_size % (2 * p.box) == 0) p.box *= 2;
-  p.nbox = C::kTile / p.box;
-  p.tile_pages = C::kTile / a.pool.page_size;
-  p.tile_rows = C::kTile % a.pool.page_size;
-  p.scale_log2 = a.sm_scale * kLog2e;
-  const int64_t qe[3] = {D, a.Hq, a.n_tokens}, qs[3] = {1, D, a.q_stride};
-  const int qb[3] = {64, p.G, p.tpt};
-  const int64_t ke[4] = {D, a.pool.page_size, a.pool.Hkv, a.pool.n_pages};
-  const int64_t ks[4] = {1, a.pool.ks[2], a.pool.ks[1], a.pool.ks[0]};
-  const int kb[4] = {64, p.box, 1, 1};
-  // V's 64-dim blocks are a dimension of their own: one box brings all of a row
-  const int64_t ve[5] = {64, a.pool.page_size, C::kDB, a.pool.Hkv, a.pool.n_pages};
-  const int64_t vs[5] = {1, a.pool.vs[2], 64, a.pool.vs[1], a.pool.vs[0]};
-  const int vb[5] = {64, p.box, C::kDB, 1, 1};
-  if (!encode(&p.q, a.Q, 3, qe, qs, qb) || !encode(&p.k, a.pool.K, 4, ke, ks, kb) ||
-      !encode(&p.v, a.pool.V, 5, ve, vs, vb))
-    return cudaErrorInvalidValue;
+  if (!paged_params<C>(a, paged_attn_tile_tokens(a.Hq / a.pool.Hkv), &p)) return cudaErrorInvalidValue;
   auto kernel = paged_attn_kernel<D, F32>;
   static int done[64] = {0};
   const cudaError_t e = set_smem_limit_once(kernel, C::kSmem, done);
