@@ -201,7 +201,8 @@ jssa_status jssa_paged_attn(const jssa_paged_layout* L, const void* Q, int64_t q
   a.part_ml = w.part_ml;
   a.counters = w.counters;
   a.rows_cap = w.rows_cap;
-  return cu(launch_paged_attn(a, num_sms_current(), static_cast<cudaStream_t>(stream)));
+  const bool few = static_cast<int64_t>(max_q_len) * (L->Hq / L->Hkv) <= kPagedFewRows;
+  return cu((few ? launch_paged_few : launch_paged_attn)(a, num_sms_current(), static_cast<cudaStream_t>(stream)));
 }
 
 jssa_status jssa_pages_fork(const jssa_paged_layout* L, const int32_t* src, const int32_t* dst, int32_t n,
