@@ -6,7 +6,8 @@
 // in one pass over K and V with a running maximum m and sum per row.  The query rows of one KV
 // head's group stand side by side: row r of a query tile is token r / G, head r % G of the group,
 // so that one tile of 128 rows serves a single token of 128 heads and 128 tokens of one head
-// alike, and a K/V row is read once for the whole group.
+// alike, and a K/V row is read once for the whole group.  (Calls of at most 16 rows per sequence and
+// KV head go to paged_few.cu.)
 //
 // Items: (sequence, KV head, block of query tiles).  An item's keys are a list of 128 (64 for
 // d = 256) at a time, its tiles: the sink pages' first rows, then the rows from the first
@@ -27,9 +28,22 @@
 // output to bf16; with an fp32 output the remainder p - bf16(p) takes a second product, so that
 // the output is good to about 2^-16.  Maxima, sums and O are fp32.
 //
-// Warps: softmax, then one that issues the MMAs, one that loads (TMA boxes of at most 128 rows
-// that never cross a page), and one that zeroes the V rows of a loaded tile that no query of
-// the item sees: P is 0 there, but such rows may hold infinities or NaN.
+// Warps: softmax; then one that issues the MMAs, one that walks the pieces and loads Q and K, one
+// that loads V (TMA boxes that never cross a page; two warps, because with 16-row pages one took
+// 3,900 cycles to issue a tile's boxes against 3,600 of the tile's work), and one that zeroes
+// the V rows of a loaded tile that no query of the item sees: P is 0 there, but such rows may
+// hold infinities or NaN.
+//
+// What bounds it, measured on a B200 (d = 128, 4 query heads per KV head): 1.1 to 1.2 PFLOP/s of
+// bf16 on prompt chunks (4 x 512 tokens at 32K: 917 us, 0.72 of the measured burst matrix rate;
+// an 8K prompt from nothing: 540 us).  A tile of two query tiles takes about 3,600 cycles for
+// 2,048 of matrix work: a row's softmax (load of S, maximum, 128 exponentials, store of P: 2,300
+// cycles while the other warpgroup shares the pipes) and its products follow one another.  Tried
+// and slower: tiles of 64 keys with two S slots per stream (the N = 64 score MMAs take as long
+// as N = 128 ones: 1,427 us against 950), four softmax warpgroups on half tiles (1,430), S read
+// twice in chunks (1,277).  The products begin with the first half of P (about 1 %), an eighth of
+// the exponentials go to the FMA pipe (983 -> 950 us; a quarter 1,012, none 983).
+//
 // Every wait is bounded; on a timeout the kernel raises DEVFLAG_TIMEOUT, all roles leave their
 // loops, copies and MMAs in flight are drained, and tensor memory is freed.
 #include <type_traits>
@@ -52,7 +66,8 @@ constexpr int kPaCubicEvery = 8;    // of so many pairs of exponentials, one goe
 template <int D>
 struct Pa {
   static constexpr int kD = D;
-  static constexpr int kItemUnits = 8;
+  static constexpr int kItemUnits = 8;                   // 2: chunks and prompts took 4 and 6 % longer
+  static constexpr bool kQueryMap = true;                // queries come by TMA
   static constexpr int kTile = D == 256 ? 64 : 128;      // keys per tile
   static constexpr int kWG = D == 256 ? 1 : 2;           // softmax warpgroups
   static constexpr int kDB = D / 64;                     // 64-dim blocks of a row
@@ -112,8 +127,8 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
   using C = Pa<D>;
   constexpr int kTile = C::kTile, kWG = C::kWG, kDB = C::kDB, kNS = C::kStages;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t q_full, q_empty, kv_full[kNS], kv_empty[kNS], edge_full[kNS], s_full[2], p_half[2], p_full[2],
-      o_full[2], piece_full[kPaPieces], piece_empty[kPaPieces], wg_bar, drain;
+  __shared__ __align__(8) uint64_t q_full, q_empty, kv_full[kNS], kv_empty[kNS], edge_full[kNS], s_full[2], p_half[2],
+      p_full[2], o_full[2], piece_full[kPaPieces], piece_empty[kPaPieces], wg_bar, drain;
   __shared__ Piece pieces[kPaPieces], late_piece;
   __shared__ uint32_t tmem_base_s, bad_s[kPaBadRing];
   __shared__ float ml_s[2][2][128];  // solo items: each warpgroup's maxima and sums
@@ -172,7 +187,8 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
     return pieces[k % kPaPieces];
   };
   auto all_ok = [&](bool x) { return __all_sync(0xFFFFFFFFu, x) != 0; };
-  auto drain_loads = [&](uint32_t used) {  // after a timeout: each load under way arrives, or has, on one of two barriers
+  // after a timeout: each load under way arrives on one of its stage's phases
+  auto drain_loads = [&](uint32_t used) {
     for (int i = 0; i < kNS; ++i)
       if ((used >> i) & 1)
         for (int t = 0; t < 2; ++t) mbar_wait_bounded(&kv_full[i], t, a.status, 1000000);
@@ -381,7 +397,8 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
               float4* to = part_word(a, D, slot_out, 8 * c) + row;
 #pragma unroll
               for (int e = 0; e < 8; ++e)
-                to[static_cast<int64_t>(e) * a.rows_cap] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                to[static_cast<int64_t>(e) * a.rows_cap] =
+                    make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
             }
           }
           __syncwarp();
@@ -637,7 +654,8 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
           for (int part = 0; part < (F32 ? 2 : 1); ++part)
 #pragma unroll
             for (int kt = k0; kt < k1; ++kt)
-              umma_bf16_ts_lo(tmem + kPaOCol + o * D, tmem + slot * C::kSCols + (kt >> 1) * 32 + part * 16 + (kt & 1) * 8,
+              umma_bf16_ts_lo(tmem + kPaOCol + o * D,
+                              tmem + slot * C::kSCols + (kt >> 1) * 32 + part * 16 + (kt & 1) * 8,
                               va + kt * (2048 >> 4) + (kt >> box_shift) * box_skip, idesc_o, part || kt ? 1u : !first);
         };
         for (int piece = 0; ok; ++piece) {

@@ -2,7 +2,8 @@
 // form, the walk over a CTA's pieces, the boxes of a tile, and the merge of cut items.
 //
 // A kernel's constants come as a class C: kD (head dim), kTile (keys per tile), kWG (query tiles of an
-// item side by side), kDB = kD / 64, kSoftmax (threads that merge), kThreads, kItemUnits.
+// item side by side), kDB = kD / 64, kSoftmax (threads that merge), kThreads, kItemUnits (what a piece
+// costs beside its tiles), kQueryMap (queries come by TMA).
 #pragma once
 
 #include <cuda.h>
@@ -484,7 +485,8 @@ inline EncodeTiled encode_tiled() {
 
 // Map of a bf16 tensor whose innermost extent is d (boxes of 64 of them, 128-byte swizzle).  The
 // stride of an extent of 1 is never used and set to a row's, which the encoder accepts.
-inline bool encode(CUtensorMap* m, const void* base, int rank, const int64_t* extent, const int64_t* stride, const int* box) {
+inline bool encode(CUtensorMap* m, const void* base, int rank, const int64_t* extent, const int64_t* stride,
+                   const int* box) {
   cuuint64_t dims[5], strides[4];
   cuuint32_t boxes[5], ones[5] = {1, 1, 1, 1, 1};
   for (int i = 0; i < rank; ++i) {
@@ -519,7 +521,7 @@ inline bool paged_params(const PagedAttnArgs& a, int tpt, PaParams* p) {
   const int64_t ve[5] = {64, a.pool.page_size, C::kDB, a.pool.Hkv, a.pool.n_pages};
   const int64_t vs[5] = {1, a.pool.vs[2], 64, a.pool.vs[1], a.pool.vs[0]};
   const int vb[5] = {64, p->box, C::kDB, 1, 1};
-  return encode(&p->q, a.Q, 3, qe, qs, qb) && encode(&p->k, a.pool.K, 4, ke, ks, kb) &&
+  return (!C::kQueryMap || encode(&p->q, a.Q, 3, qe, qs, qb)) && encode(&p->k, a.pool.K, 4, ke, ks, kb) &&
          encode(&p->v, a.pool.V, 5, ve, vs, vb);
 }
 

@@ -5,6 +5,12 @@
 // [n_pages] and the sequence lengths [B].  Every result is a function of the state and the
 // arguments alone (the lowest free pages are taken, in sequence order), so the kernels use
 // scans where order matters and atomics only for counts, whose sums do not depend on it.
+//
+// Measured on a B200 (device time of a launch on its own; an empty one takes 4 us).  Serving-size book, 256
+// or 128 sequences, 8,192 pages: fork 5.4 us, reserve 12.3, release 6.1, compact 12.3: chains of a few
+// dependent reads each, so each is one launch of one block (reserve), a block per row, or one cluster
+// (compact).  Page copies: 2,000 pages of 256 KB in 169 us, 0.97 of the measured copy rate; 180 in 18
+// us.  Append of 25,000 rows of 8 heads 39-41 us (5.2 TB/s), of 64 rows 7.4.
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -253,8 +259,8 @@ __global__ void __launch_bounds__(256) pages_release_kernel(PageBook k, const in
 // where the table has few entries, by a second one over the whole GPU otherwise.
 constexpr int kCompactBlocks = 8;
 constexpr int64_t kCompactEntries = 1 << 16;  // 8 passes of the cluster's threads
-__device__ __forceinline__ void remap_entries(const PageBook& k, const int32_t* dst, const int32_t* map, int m, int64_t i0,
-                                              int64_t step) {
+__device__ __forceinline__ void remap_entries(const PageBook& k, const int32_t* dst, const int32_t* map, int m,
+                                              int64_t i0, int64_t step) {
   const int64_t n = static_cast<int64_t>(k.B) * k.max_pages;
   for (int64_t i = i0; i < n; i += step) {
     const int p = k.table[i];
@@ -420,8 +426,8 @@ __global__ void __launch_bounds__(256) paged_append_kernel(PagedAppendArgs a) {
       const int e = is_v ? rest - per : rest;
       const int64_t(&st)[3] = is_v ? a.pool.vs : a.pool.ks;
       x[u] = __ldcs(reinterpret_cast<const uint4*>(is_v ? a.V_new : a.K_new) + (i0 + j) * (a.new_stride >> 3) + e);
-      to[u] = reinterpret_cast<uint4*>(is_v ? a.pool.V : a.pool.K) + page_s[j] * (st[0] >> 3) + (e / cpr) * (st[1] >> 3) +
-              row_s[j] * (st[2] >> 3) + e % cpr;
+      to[u] = reinterpret_cast<uint4*>(is_v ? a.pool.V : a.pool.K) + page_s[j] * (st[0] >> 3) +
+              (e / cpr) * (st[1] >> 3) + row_s[j] * (st[2] >> 3) + e % cpr;
     }
 #pragma unroll
     for (int u = 0; u < kAppendPer; ++u)
