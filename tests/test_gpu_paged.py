@@ -130,6 +130,11 @@ CASES = [
     dict(lens=[2000, 40], nq=[8, 5], d=256, G=1, window=16, sinks=33, page=16),
     dict(lens=[600, 601, 602], nq=[2, 0, 4], G=8, Hkv=1, window=1, sinks=1, tail=3),
     dict(lens=[600, 700], nq=[2, 4], G=8, Hkv=1, window=1, sinks=0),
+    dict(lens=[900, 18, 333], nq=[17, 17, 2], d=64, Hkv=2, G=1, window=100, sinks=20, page=48),
+    dict(lens=[700, 16, 2000], nq=[16, 16, 9], d=64, G=2, page=32, fused=True),
+    dict(lens=[1300, 31, 65], nq=[4, 1, 3], G=8, Hkv=1, window=70, sinks=3, page=16, tail=2),
+    dict(lens=[1300, 31, 65], nq=[1, 1, 0], G=27, Hkv=2, page=80),
+    dict(lens=[800, 20], nq=[16, 3], d=256, Hkv=2, G=1, window=40, sinks=17, page=16),
     # chunks and whole prompts
     dict(lens=[257], nq=[257], Hkv=1, G=1),
     dict(lens=[513, 64, 1], nq=[513, 64, 1], d=64, G=2, page=32),

@@ -201,7 +201,7 @@ jssa_status jssa_paged_attn(const jssa_paged_layout* L, const void* Q, int64_t q
   a.part_ml = w.part_ml;
   a.counters = w.counters;
   a.rows_cap = w.rows_cap;
-  const bool few = static_cast<int64_t>(max_q_len) * (L->Hq / L->Hkv) <= kPagedFewRows;
+  const bool few = paged_few_rows(L->d, static_cast<int64_t>(max_q_len) * (L->Hq / L->Hkv));
   return cu((few ? launch_paged_few : launch_paged_attn)(a, num_sms_current(), static_cast<cudaStream_t>(stream)));
 }
 

@@ -280,7 +280,7 @@ struct PagedAttnArgs {
 int paged_attn_tile_tokens(int G);
 int paged_attn_rows(int d, int G, int64_t max_q_len);  // rows of an item, at most
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, int num_sms, cudaStream_t s);
-constexpr int kPagedFewRows = 16;  // rows of a sequence and KV head that the kernel below takes, at most
+bool paged_few_rows(int d, int64_t rows);  // whether the kernel below takes so many rows of a sequence and KV head
 cudaError_t launch_paged_few(const PagedAttnArgs& a, int num_sms, cudaStream_t s);
 
 }  // namespace jssa

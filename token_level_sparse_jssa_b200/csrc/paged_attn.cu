@@ -6,8 +6,8 @@
 // in one pass over K and V with a running maximum m and sum per row.  The query rows of one KV
 // head's group stand side by side: row r of a query tile is token r / G, head r % G of the group,
 // so that one tile of 128 rows serves a single token of 128 heads and 128 tokens of one head
-// alike, and a K/V row is read once for the whole group.  (Calls of at most 16 rows per sequence and
-// KV head go to paged_few.cu.)
+// alike, and a K/V row is read once for the whole group.  (Calls of few rows per sequence and KV
+// head go to paged_few.cu.)
 //
 // Items: (sequence, KV head, block of query tiles).  An item's keys are a list of 128 (64 for
 // d = 256) at a time, its tiles: the sink pages' first rows, then the rows from the first

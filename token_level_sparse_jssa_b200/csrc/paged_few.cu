@@ -1,5 +1,5 @@
 // Attention over a paged cache for few query rows: a KV head's group and new tokens of a sequence
-// together fill at most 16 rows (decode, and a few speculated tokens of small groups).
+// together fill at most 16 rows, 32 for d = 64 (decode, and a few speculated tokens).
 //
 // Such a call is bound by the bytes of K and V.  On the 128-row tiles of the large kernel it would
 // spend 8 to 128 times the matrix work that it needs (whose power lowers the clock: one token over
@@ -26,11 +26,13 @@
 namespace jssa {
 namespace {
 
-template <int D>
+// MT: row tiles of 16.
+template <int D, int MT>
 struct Few {
   static constexpr int kD = D;
   static constexpr int kItemUnits = 4;
   static constexpr bool kQueryMap = false;
+  static constexpr int kRows = 16 * MT;
   static constexpr int kTile = D == 256 ? 64 : 128;
   static constexpr int kWG = 1;
   static constexpr int kDB = D / 64;
@@ -39,21 +41,21 @@ struct Few {
   static constexpr int kCols = D / kDimWarps;            // output columns of a warp
   static constexpr int kHalfStage = kTile * D * 2;       // K or V of a tile
   static constexpr int kStages = D == 64 ? 5 : 3;
-  static constexpr int kSumBytes = 4 * 16 * kCols * 4;   // half the warps' output rows
+  static constexpr int kSumBytes = 4 * kRows * kCols * 4;   // half the warps' output rows
   static constexpr int kSmem = 2 * kStages * kHalfStage + kSumBytes;
   static constexpr int kSoftmax = 256;
   static constexpr int kThreads = kSoftmax + 32;
 };
 
-template <int D, bool F32>
-__global__ void __launch_bounds__(Few<D>::kThreads, 1) paged_few_kernel(const __grid_constant__ PaParams p) {
-  using C = Few<D>;
+template <int D, bool F32, int MT>
+__global__ void __launch_bounds__((Few<D, MT>::kThreads), 1) paged_few_kernel(const __grid_constant__ PaParams p) {
+  using C = Few<D, MT>;
   constexpr int kTile = C::kTile, kDB = C::kDB, kNS = C::kStages, kCols = C::kCols, kKeyWarps = C::kKeyWarps;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t full[kNS], empty[kNS], piece_full[kPaPieces], piece_empty[kPaPieces], all_bar;
   __shared__ Piece pieces[kPaPieces], late_piece;
   __shared__ uint32_t bad_s[kPaBadRing];
-  __shared__ float m_s[8][16], l_s[8][16];
+  __shared__ float m_s[8][C::kRows], l_s[8][C::kRows];
   __shared__ int dead_s, last_s;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -151,7 +153,7 @@ __global__ void __launch_bounds__(Few<D>::kThreads, 1) paged_few_kernel(const __
   } else {
     // ------------------------------------------------------------------ attention
     const int kw = warp % kKeyWarps, dw = warp / kKeyWarps;  // this warp's keys and columns
-    const int r0 = lane >> 2, c2 = (lane & 3) * 2;           // its rows r0 and r0 + 8, its columns c2, c2 + 1 of 8
+    const int r0 = lane >> 2, c2 = (lane & 3) * 2;           // its rows r0, r0 + 8, ..., its columns c2, c2 + 1 of 8
     uint32_t st = 0, st_par = 0, tiles = 0, all_par = 0;
     bool ok = true;
     auto meet = [&]() {
@@ -166,44 +168,54 @@ __global__ void __launch_bounds__(Few<D>::kThreads, 1) paged_few_kernel(const __
       const Piece& s = pieces[piece % kPaPieces];
       if (!ok || s.t1 == 0) break;
       const int rows = s.it.ntok * p.G;
-      uint32_t q[D / 16][4];
-      int va[2], vb[2], vc[2];
+      uint32_t q[MT][D / 16][4];
+      int pos[2 * MT];
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        const int r = r0 + 8 * y, tok = min(r / p.G, s.it.ntok - 1), pos = s.it.pf + tok;
-        va[y] = a.window > 0 ? min(a.n_sinks, pos + 1) : 0;
-        vb[y] = (a.window > 0 ? max(0, pos + 1 - a.window) : 0) - s.it.shift;
-        vc[y] = pos + 1 - s.it.shift;
+      for (int y = 0; y < 2 * MT; ++y) {
+        const int r = r0 + 8 * y, tok = min(r / p.G, s.it.ntok - 1);
+        pos[y] = s.it.pf + tok;
         const uint32_t* src = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(a.Q) +
                                                                 (s.q0 + tok) * a.q_stride +
                                                                 static_cast<int64_t>(s.h * p.G + r % p.G) * D + c2);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          q[kk][y] = r < rows ? __ldg(src + kk * 8) : 0u;
-          q[kk][2 + y] = r < rows ? __ldg(src + kk * 8 + 4) : 0u;
+          q[y >> 1][kk][y & 1] = r < rows ? __ldg(src + kk * 8) : 0u;
+          q[y >> 1][kk][2 + (y & 1)] = r < rows ? __ldg(src + kk * 8 + 4) : 0u;
         }
       }
       const int pl = s.it.pf + s.it.ntok - 1;
       const int b_max = (a.window > 0 ? max(0, pl + 1 - a.window) : 0) - s.it.shift, c_min = s.it.pf + 1 - s.it.shift;
-      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-      float o[kCols / 8][4];
+      float m[2 * MT], l[2 * MT];
+      float o[MT][kCols / 8][4];
 #pragma unroll
-      for (int n = 0; n < kCols / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+      for (int t = 0; t < MT; ++t) {
+        m[2 * t] = m[2 * t + 1] = -INFINITY;
+        l[2 * t] = l[2 * t + 1] = 0.f;
+#pragma unroll
+        for (int n = 0; n < kCols / 8; ++n) o[t][n][0] = o[t][n][1] = o[t][n][2] = o[t][n][3] = 0.f;
+      }
       for (int i = s.t0; i < s.t1; ++i) {
         ok = all_ok(wait(&full[st], st_par));
         if (!ok) break;
         const uint32_t k_at = kv_s + 2 * st * C::kHalfStage, v_at = k_at + C::kHalfStage;
         const int k0 = 16 * kw, v0 = i * kTile + k0;
         // scores of keys k0 .. k0 + 15
-        float x[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        float x[MT][2][4];
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[t][0][e] = x[t][1][e] = 0.f;
         {
           const int key = k0 + (lane >> 4) * 8 + (lane & 7), ch = (lane >> 3) & 1;
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             uint32_t b[4];
             ldmatrix_x4_at(b, k_at + (kk >> 2) * (kTile * 128) + key * 128 + ((((kk & 3) * 2 + ch) ^ (key & 7)) << 4));
-            mma_bf16_16816(x[0], q[kk], b[0], b[1]);
-            mma_bf16_16816(x[1], q[kk], b[2], b[3]);
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+              mma_bf16_16816(x[t][0], q[t][kk], b[0], b[1]);
+              mma_bf16_16816(x[t][1], q[t][kk], b[2], b[3]);
+            }
           }
         }
         const uint32_t bad = bad_s[tiles % kPaBadRing];
@@ -215,57 +227,65 @@ __global__ void __launch_bounds__(Few<D>::kThreads, 1) paged_few_kernel(const __
           for (int n = 0; n < 2; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const int v = v0 + 8 * n + c2 + e;
+              const int v = v0 + 8 * n + c2 + e, t = v < s.it.s_al ? v : v + s.it.shift;  // place and token
 #pragma unroll
-              for (int y = 0; y < 2; ++y)
-                if (lost || !(v < va[y] || (v >= vb[y] && v < vc[y]))) x[n][2 * y + e] = -INFINITY;
+              for (int y = 0; y < 2 * MT; ++y) {
+                const bool seen = !lost && t <= pos[y] && (a.window == 0 || t > pos[y] - a.window || t < a.n_sinks);
+                if (!seen) x[y >> 1][n][2 * (y & 1) + e] = -INFINITY;
+              }
               if (lost || v >= s.it.nv || (v >= s.it.z0 && v < s.it.z1)) keep[n] &= e ? 0x0000FFFFu : 0xFFFF0000u;
             }
         }
         // each row's maximum over the warp's keys; the output is rescaled when it grows by more than 2^8
-        float mx[2];
+        float mx[2 * MT];
         bool move = false;
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          mx[y] = fmaxf(fmaxf(x[0][2 * y], x[0][2 * y + 1]), fmaxf(x[1][2 * y], x[1][2 * y + 1]));
+        for (int y = 0; y < 2 * MT; ++y) {
+          const float(&z)[2][4] = x[y >> 1];
+          const int e = 2 * (y & 1);
+          mx[y] = fmaxf(fmaxf(z[0][e], z[0][e + 1]), fmaxf(z[1][e], z[1][e + 1]));
           mx[y] = fmaxf(mx[y], __shfl_xor_sync(0xFFFFFFFFu, mx[y], 1));
           mx[y] = fmaxf(mx[y], __shfl_xor_sync(0xFFFFFFFFu, mx[y], 2));
           move |= m[y] == -INFINITY ? mx[y] > -INFINITY : (mx[y] - m[y]) * p.scale_log2 > 8.f;
         }
         if (__any_sync(0xFFFFFFFFu, move)) {
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
+          for (int y = 0; y < 2 * MT; ++y) {
             const float mn = fmaxf(m[y], mx[y]);
             const float w = m[y] == -INFINITY ? 0.f : exp2_approx((m[y] - mn) * p.scale_log2);
             m[y] = mn;
             l[y] *= w;
 #pragma unroll
             for (int n = 0; n < kCols / 8; ++n) {
-              o[n][2 * y] *= w;
-              o[n][2 * y + 1] *= w;
+              o[y >> 1][n][2 * (y & 1)] *= w;
+              o[y >> 1][n][2 * (y & 1) + 1] *= w;
             }
           }
         }
-        float pr[2][4];
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
+        for (int y = 0; y < 2 * MT; ++y) {
           const float mm = m[y] == -INFINITY ? 0.f : m[y] * p.scale_log2;
 #pragma unroll
           for (int n = 0; n < 2; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              pr[n][2 * y + e] = exp2_approx(fmaf(x[n][2 * y + e], p.scale_log2, -mm));
-              l[y] += pr[n][2 * y + e];
+              float& z = x[y >> 1][n][2 * (y & 1) + e];
+              z = exp2_approx(fmaf(z, p.scale_log2, -mm));
+              l[y] += z;
             }
         }
-        uint32_t hi[4], lo[4];
+        uint32_t hi[MT][4];
+        [[maybe_unused]] uint32_t lo[MT][4];
 #pragma unroll
-        for (int f = 0; f < 4; ++f) {  // A fragment: row r0 + 8 (f & 1), keys c2, c2 + 1 of half f >> 1
-          const float p0 = pr[f >> 1][2 * (f & 1)], p1 = pr[f >> 1][2 * (f & 1) + 1];
-          hi[f] = pack_bf16x2(p0, p1);
-          if constexpr (F32)
-            lo[f] = pack_bf16x2(p0 - bf16_bits_to_float(hi[f] & 0xFFFFu), p1 - __uint_as_float(hi[f] & 0xFFFF0000u));
-        }
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+          for (int f = 0; f < 4; ++f) {  // A fragment: row r0 + 8 (f & 1), keys c2, c2 + 1 of half f >> 1
+            const float p0 = x[t][f >> 1][2 * (f & 1)], p1 = x[t][f >> 1][2 * (f & 1) + 1];
+            hi[t][f] = pack_bf16x2(p0, p1);
+            if constexpr (F32)
+              lo[t][f] =
+                  pack_bf16x2(p0 - bf16_bits_to_float(hi[t][f] & 0xFFFFu), p1 - __uint_as_float(hi[t][f] & 0xFFFF0000u));
+          }
         {
           const int key = ((lane >> 3) & 1) * 8 + (lane & 7);
           const uint32_t vb_at = v_at + (k0 / p.box) * p.box * (kDB * 128) + (k0 % p.box) * 128 + key * 128;
@@ -275,11 +295,14 @@ __global__ void __launch_bounds__(Few<D>::kThreads, 1) paged_few_kernel(const __
             uint32_t b[4];
             ldmatrix_x4_trans_at(b, vb_at + (ch >> 3) * p.box * 128 + (((ch & 7) ^ (key & 7)) << 4));
             if (edge) b[0] &= keep[0], b[1] &= keep[1], b[2] &= keep[0], b[3] &= keep[1];
-            mma_bf16_16816(o[2 * n], hi, b[0], b[1]);
-            mma_bf16_16816(o[2 * n + 1], hi, b[2], b[3]);
-            if constexpr (F32) {
-              mma_bf16_16816(o[2 * n], lo, b[0], b[1]);
-              mma_bf16_16816(o[2 * n + 1], lo, b[2], b[3]);
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+              mma_bf16_16816(o[t][2 * n], hi[t], b[0], b[1]);
+              mma_bf16_16816(o[t][2 * n + 1], hi[t], b[2], b[3]);
+              if constexpr (F32) {
+                mma_bf16_16816(o[t][2 * n], lo[t], b[0], b[1]);
+                mma_bf16_16816(o[t][2 * n + 1], lo[t], b[2], b[3]);
+              }
             }
           }
         }
@@ -291,7 +314,7 @@ __global__ void __launch_bounds__(Few<D>::kThreads, 1) paged_few_kernel(const __
       if (!ok) break;
       // ---- the warps' rows on one maximum, then their sums
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {
+      for (int y = 0; y < 2 * MT; ++y) {
         l[y] += __shfl_xor_sync(0xFFFFFFFFu, l[y], 1);
         l[y] += __shfl_xor_sync(0xFFFFFFFFu, l[y], 2);
         if (m[y] == -INFINITY) l[y] = 0.f;
@@ -306,24 +329,25 @@ __global__ void __launch_bounds__(Few<D>::kThreads, 1) paged_few_kernel(const __
         return M;
       };
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {
+      for (int y = 0; y < 2 * MT; ++y) {
         const float M = row_max(r0 + 8 * y);
         const float w = m[y] == -INFINITY ? 0.f : exp2_approx((m[y] - M) * p.scale_log2);
 #pragma unroll
         for (int n = 0; n < kCols / 8; ++n) {
-          o[n][2 * y] *= w;
-          o[n][2 * y + 1] *= w;
+          o[y >> 1][n][2 * (y & 1)] *= w;
+          o[y >> 1][n][2 * (y & 1) + 1] *= w;
         }
       }
       // four warps' worth of room: the upper half of the key warps hands its rows down, then the rest of them
       constexpr int kHalf = kKeyWarps / 2;
-      auto room = [&](int k, int r, int c) { return sum_s + ((k * C::kDimWarps + dw) * 16 + r) * kCols + c; };
+      auto room = [&](int k, int r, int c) { return sum_s + ((k * C::kDimWarps + dw) * C::kRows + r) * kCols + c; };
       auto put = [&](int k) {
 #pragma unroll
         for (int n = 0; n < kCols / 8; ++n)
 #pragma unroll
-          for (int y = 0; y < 2; ++y)
-            *reinterpret_cast<float2*>(room(k, r0 + 8 * y, 8 * n + c2)) = make_float2(o[n][2 * y], o[n][2 * y + 1]);
+          for (int y = 0; y < 2 * MT; ++y)
+            *reinterpret_cast<float2*>(room(k, r0 + 8 * y, 8 * n + c2)) =
+                make_float2(o[y >> 1][n][2 * (y & 1)], o[y >> 1][n][2 * (y & 1) + 1]);
       };
       if (kw >= kHalf) put(kw - kHalf);
       ok = meet();
@@ -332,10 +356,10 @@ __global__ void __launch_bounds__(Few<D>::kThreads, 1) paged_few_kernel(const __
 #pragma unroll
         for (int n = 0; n < kCols / 8; ++n)
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
+          for (int y = 0; y < 2 * MT; ++y) {
             const float2 t = *reinterpret_cast<const float2*>(room(kw, r0 + 8 * y, 8 * n + c2));
-            o[n][2 * y] += t.x;
-            o[n][2 * y + 1] += t.y;
+            o[y >> 1][n][2 * (y & 1)] += t.x;
+            o[y >> 1][n][2 * (y & 1) + 1] += t.y;
           }
         put(kw);
       }
@@ -348,7 +372,7 @@ __global__ void __launch_bounds__(Few<D>::kThreads, 1) paged_few_kernel(const __
         float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int k = 0; k < kHalf; ++k) {
-          const float* from = sum_s + ((k * C::kDimWarps + d0) * 16 + r) * kCols + c % kCols;
+          const float* from = sum_s + ((k * C::kDimWarps + d0) * C::kRows + r) * kCols + c % kCols;
           const float4 y = *reinterpret_cast<const float4*>(from);
           t.x += y.x, t.y += y.y, t.z += y.z, t.w += y.w;
         }
@@ -397,25 +421,35 @@ __global__ void __launch_bounds__(Few<D>::kThreads, 1) paged_few_kernel(const __
   __syncthreads();
 }
 
-template <int D, bool F32>
+template <int D, bool F32, int MT>
 cudaError_t launch(const PagedAttnArgs& a, int num_sms, cudaStream_t s) {
-  using C = Few<D>;
+  using C = Few<D, MT>;
   PaParams p{};
-  if (!paged_params<C>(a, kPagedFewRows / (a.Hq / a.pool.Hkv), &p)) return cudaErrorInvalidValue;
-  auto kernel = paged_few_kernel<D, F32>;
+  if (!paged_params<C>(a, C::kRows / (a.Hq / a.pool.Hkv), &p)) return cudaErrorInvalidValue;
+  auto kernel = paged_few_kernel<D, F32, MT>;
   static int done[64] = {0};
   const cudaError_t e = set_smem_limit_once(kernel, C::kSmem, done);
   if (e != cudaSuccess) return e;
   return launch_ex(kernel, dim3(num_sms), dim3(C::kThreads), C::kSmem, s, 0, p);
 }
 
+template <int D, int MT>
+cudaError_t launch(const PagedAttnArgs& a, int num_sms, cudaStream_t s) {
+  return a.out_bf16 ? launch<D, false, MT>(a, num_sms, s) : launch<D, true, MT>(a, num_sms, s);
+}
+
 }  // namespace
 
+// Two row tiles pay for d = 64 only: 8 tokens of 4-head groups over 16 caches of 8K-16K rows took 59 us here and
+// 62 in the large kernel; for d = 128, where a tile must shrink to 64 keys, over 8 caches of 5K 69 and 49.
+bool paged_few_rows(int d, int64_t rows) { return rows <= (d == 64 ? 32 : 16); }
+
 cudaError_t launch_paged_few(const PagedAttnArgs& a, int num_sms, cudaStream_t s) {
+  const bool one = static_cast<int64_t>(a.max_q_len) * (a.Hq / a.pool.Hkv) <= 16;
   switch (a.pool.d) {
-    case 64: return a.out_bf16 ? launch<64, false>(a, num_sms, s) : launch<64, true>(a, num_sms, s);
-    case 128: return a.out_bf16 ? launch<128, false>(a, num_sms, s) : launch<128, true>(a, num_sms, s);
-    case 256: return a.out_bf16 ? launch<256, false>(a, num_sms, s) : launch<256, true>(a, num_sms, s);
+    case 64: return one ? launch<64, 1>(a, num_sms, s) : launch<64, 2>(a, num_sms, s);
+    case 128: return launch<128, 1>(a, num_sms, s);
+    case 256: return launch<256, 1>(a, num_sms, s);
   }
   return cudaErrorNotSupported;
 }
