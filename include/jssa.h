@@ -345,7 +345,8 @@ JSSA_API jssa_status jssa_calibrate(const jssa_layout* L, const void* Qc, const 
  * may have none.  Rows at and past q_begin[B] are neither read nor written.
  *
  * Workspace: jssa_paged_workspace_size() bytes, zeroed once with jssa_workspace_init(); it holds
- * the status word and scratch, and every call leaves it ready for the next.  Calls that may
+ * the status word and scratch, and every call leaves it ready for the next, of another layout
+ * too: one of the largest size serves several layouts in turn.  Calls that may
  * overlap on the GPU (other streams) need a workspace each.
  *
  * Checks on the device: a sequence whose length is outside [0, max_pages * page_size], or whose

@@ -268,6 +268,74 @@ def test_pools_inside_one_tensor(d):
     assert bool(both[:, 0, :, :, d:].isnan().all()) and bool(both[:, 1, :, :, :8].isnan().all())
 
 
+@pytest.mark.parametrize("kw", [
+    dict(lens=[300], nq=[3], d=256, Hkv=1, G=128, page=48),
+    dict(lens=[1000, 300], nq=[1, 2], d=64, Hkv=2, G=128, page=64, window=77, sinks=9),
+    dict(lens=[16], nq=[16], d=64, Hkv=1, G=1, page=16, extra_cols=0),
+    dict(lens=[500, 200], nq=[1, 200], window=2 ** 31 - 1, sinks=2 ** 31 - 1),
+    dict(lens=[500, 200], nq=[1, 200], window=50, sinks=2 ** 31 - 1),
+    dict(lens=[500, 200], nq=[1, 2], window=50, sinks=2 ** 31 - 1, G=2),
+])
+def test_extremes(kw):
+    for out in (torch.bfloat16, torch.float32):
+        p = Problem(**kw, out=out)
+        p.run()
+        p.check()
+
+
+def test_bounds_on_new_tokens_may_be_generous():
+    # max_q_len far above what the sequences bring: the large kernel for single tokens
+    for lens, nq in (([700, 20, 5000], [1, 1, 1]), ([700, 20], [30, 2])):
+        p = Problem(lens, nq, page=32)
+        p.max_q = 100000
+        p.ws = jssa.alloc_paged_workspace(p.L, p.max_q)
+        p.run()
+        p.check()
+
+
+def test_rows_before_the_first_sequence_are_left():
+    for nq in ([1, 2, 1], [40, 1, 130]):
+        p = Problem([700, 20, 300], nq, tail=5)
+        q, o, lse = p.Q, p.O, p.lse
+        pad = torch.full_like(q[:3], float("nan"))
+        p.Q = torch.cat([pad, q])
+        p.O, p.lse = torch.cat([o[:3], o]), torch.cat([lse[:3], lse])
+        p.q_begin += 3
+        p.run()
+        assert bool((p.O[:3] == -777.0).all()) and bool((p.lse[:3] == -777.0).all())
+        p.Q, p.O, p.lse = q, p.O[3:], p.lse[3:]
+        p.check()
+
+
+def test_one_workspace_for_several_layouts():
+    a, b = Problem([5000, 40], [1, 1], seed=4), Problem([900, 300, 8], [300, 1, 8], d=64, Hkv=1, G=2, page=48, seed=6)
+    ws = max(a.ws, b.ws, key=len)
+    a.ws = b.ws = ws
+    K = torch.zeros(3000, 1, 16, 64, dtype=torch.bfloat16, device="cuda")
+    book = Book(50, 20, 3000, 16)
+    table, ref, lens = _state(book)
+    L = jssa.make_paged_layout(K, K, table, 1)
+    assert len(ws) >= jssa.paged_workspace_size(L)
+    src, dst = i32([0] * 50), i32([0] * 50)
+    r = random.Random(3)
+    for step in range(6):
+        n_new = [r.choice((0, 1, 7, 33)) for _ in range(50)]
+        got = book.reserve(n_new)
+        jssa.pages_reserve(L, i32(n_new), table, ref, lens, src, dst, ws)
+        assert (src.tolist(), dst.tolist()) == got
+        if step == 2:
+            book.release([int(b % 3 == 0) for b in range(50)], 0, 0)
+            jssa.pages_release(L, i32([int(b % 3 == 0) for b in range(50)]), 0, 0, table, ref, lens, ws)
+            held = [b for b in range(50) if book.lens[b]]
+            book.fork(held[:10], [0, 3, 6, 9, 12, 15, 18, 21, 24, 27])
+            jssa.pages_fork(L, i32(held[:10]), i32([0, 3, 6, 9, 12, 15, 18, 21, 24, 27]), table, ref, lens, ws)
+        for p in (a, b):
+            p.O.fill_(-777.0)
+            p.run()
+            p.check()
+        _same(book, table, ref, lens)
+
+
 def test_many_pieces_and_many_sequences():
     # one item cut over the whole GPU; more sequences than the GPU has multiprocessors, most of one tile
     p = Problem([40000], [1], Hkv=1, G=2, page=64, out=torch.float32)

@@ -36,10 +36,10 @@ jssa_status check_paged(const jssa_paged_layout* L) {
 
 struct PagedWorkspace {
   int* status;
-  int32_t* growers;    // [n_pages, 2], zero between calls
+  int32_t* counters;   // [num_sms], zero between calls; at the same place for every layout
+  int32_t* growers;    // [n_pages, 2]
   int32_t* free_list;  // [n_pages]
   int32_t* map;        // [n_pages + 1]
-  int32_t* counters;   // [num_sms], zero between calls
   float2* part_ml;     // [2 num_sms][rows_cap]
   float* part_o;       // [2 num_sms][rows_cap][d]
   int rows_cap;
@@ -58,10 +58,10 @@ jssa_status carve_paged(const jssa_paged_layout* L, int max_q_len, void* base, P
   };
   const size_t n = static_cast<size_t>(L->n_pages);
   w->status = reinterpret_cast<int*>(take(sizeof(int)));
+  w->counters = reinterpret_cast<int32_t*>(take(num_sms * sizeof(int32_t)));
   w->growers = reinterpret_cast<int32_t*>(take(2 * n * sizeof(int32_t)));
   w->free_list = reinterpret_cast<int32_t*>(take(n * sizeof(int32_t)));
   w->map = reinterpret_cast<int32_t*>(take((n + 1) * sizeof(int32_t)));
-  w->counters = reinterpret_cast<int32_t*>(take(num_sms * sizeof(int32_t)));
   w->rows_cap = paged_attn_rows(L->d, L->Hq / L->Hkv, max_q_len);
   const size_t rows = static_cast<size_t>(2 * num_sms) * w->rows_cap;
   w->part_ml = reinterpret_cast<float2*>(take(rows * sizeof(float2)));

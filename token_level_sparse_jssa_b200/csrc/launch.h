@@ -246,7 +246,7 @@ struct PagedAppendArgs {
 };
 cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t s);
 cudaError_t launch_pages_fork(const PageBook& k, const int32_t* src, const int32_t* dst, int n, cudaStream_t s);
-// growers: [n_pages, 2] zero on entry and exit; free_list: [n_pages]
+// growers: [n_pages, 2]; free_list: [n_pages]
 cudaError_t launch_pages_reserve(const PageBook& k, const int32_t* n_new, int32_t* copy_src, int32_t* copy_dst,
                                  int32_t* growers, int32_t* free_list, cudaStream_t s);
 cudaError_t launch_pages_release(const PageBook& k, const int32_t* ended, int window, int n_sinks, cudaStream_t s);

@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(256) pages_fork_kernel(PageBook k, const int32
 // One block; thread b plans sequence b (B <= 1024).  A shared partly filled page with count r
 // and m growers is given up by every grower but, when m = r, the last one (sequence by
 // sequence, each that leaves lowers the count, and the last finds itself alone): m and the
-// highest grower come from two atomics per page in `growers`, cleared again before the end.
+// highest grower come from two atomics per page in `growers`, cleared before them.
 // The free pages are listed in ascending order until enough are found: a pass takes 16 x 1024
 // counts, a ballot per 32 of them, and one scan over the 512 ballots ranks them all.  The first
 // 4096 stay in shared memory.  Then a warp per sequence writes the entries.
@@ -134,6 +134,11 @@ __global__ void __launch_bounds__(1024) pages_reserve_kernel(PageBook k, const i
       }
     }
   }
+  if (part_page) {
+    growers[2 * static_cast<int64_t>(last)] = 0;
+    growers[2 * static_cast<int64_t>(last) + 1] = 0;
+  }
+  __threadfence_block();
   fail = __syncthreads_or(fail) != 0;
   if (!fail && part_page) {
     atomicAdd(growers + 2 * static_cast<int64_t>(last), 1);
@@ -147,11 +152,6 @@ __global__ void __launch_bounds__(1024) pages_reserve_kernel(PageBook k, const i
     const int m = __ldcg(growers + 2 * static_cast<int64_t>(last));
     const int top = __ldcg(growers + 2 * static_cast<int64_t>(last) + 1);
     split = r > 1 && (m < r || top != b + 1);
-  }
-  __syncthreads();
-  if (!fail && part_page) {
-    growers[2 * static_cast<int64_t>(last)] = 0;
-    growers[2 * static_cast<int64_t>(last) + 1] = 0;
   }
   int lo = 0, cnt = 0;
   if (!fail && add > 0) {
