@@ -40,6 +40,7 @@ struct PagedWorkspace {
   int32_t* growers;    // [n_pages, 2]
   int32_t* free_list;  // [n_pages]
   int32_t* map;        // [n_pages + 1]
+  PagedCut* cuts;      // [num_sms]
   float2* part_ml;     // [2 num_sms][rows_cap]
   float* part_o;       // [2 num_sms][rows_cap][d]
   int rows_cap;
@@ -62,6 +63,7 @@ jssa_status carve_paged(const jssa_paged_layout* L, int max_q_len, void* base, P
   w->growers = reinterpret_cast<int32_t*>(take(2 * n * sizeof(int32_t)));
   w->free_list = reinterpret_cast<int32_t*>(take(n * sizeof(int32_t)));
   w->map = reinterpret_cast<int32_t*>(take((n + 1) * sizeof(int32_t)));
+  w->cuts = reinterpret_cast<PagedCut*>(take(num_sms * sizeof(PagedCut)));
   w->rows_cap = paged_attn_rows(L->d, L->Hq / L->Hkv, max_q_len);
   const size_t rows = static_cast<size_t>(2 * num_sms) * w->rows_cap;
   w->part_ml = reinterpret_cast<float2*>(take(rows * sizeof(float2)));
@@ -200,6 +202,7 @@ jssa_status jssa_paged_attn(const jssa_paged_layout* L, const void* Q, int64_t q
   a.part_o = w.part_o;
   a.part_ml = w.part_ml;
   a.counters = w.counters;
+  a.cuts = w.cuts;
   a.rows_cap = w.rows_cap;
   const bool few = paged_few_rows(L->d, static_cast<int64_t>(max_q_len) * (L->Hq / L->Hkv));
   return cu((few ? launch_paged_few : launch_paged_attn)(a, num_sms_current(), static_cast<cudaStream_t>(stream)));

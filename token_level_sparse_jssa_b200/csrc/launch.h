@@ -256,6 +256,11 @@ cudaError_t launch_pages_compact(const PageBook& k, int32_t* src, int32_t* dst, 
 cudaError_t launch_pages_copy(const PagePool& p, const int32_t* src, const int32_t* dst, int n, const int32_t* count,
                               int* status, int num_sms, cudaStream_t s);
 
+// An item that was cut after its first CTA: its rows and pieces, for the merge launch (pieces 0: none).
+struct PagedCut {
+  int64_t q0;  // first token's row
+  int rows, h, pieces;
+};
 struct PagedAttnArgs {
   PagePool pool;
   const void* Q;
@@ -275,6 +280,7 @@ struct PagedAttnArgs {
   float* part_o;
   float2* part_ml;
   int32_t* counters;
+  PagedCut* cuts;  // [num_sms]
   int rows_cap;
 };
 int paged_attn_tile_tokens(int G);

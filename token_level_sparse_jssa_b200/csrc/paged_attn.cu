@@ -14,8 +14,10 @@
 // query's window to the last query.  All tiles of all items form one line that is cut into equal
 // pieces, one per CTA (one CTA per SM): long caches with few rows are split, ragged batches are
 // balanced, and the host needs no lengths.  An item that is cut leaves unnormalised partial
-// outputs with their maxima and sums in the workspace; the CTA that finishes it last merges
-// them, in the order of the cuts, so results do not depend on timing.
+// outputs with their maxima and sums in the workspace.  They are merged in the order of the cuts, so
+// results do not depend on timing: items of many rows by a second launch, whose blocks come as CTAs
+// leave (the last CTA alone took 2 us per piece: 500 tokens of one head over 40K keys 79 us, now 42),
+// the others by the CTA that finishes them last.
 //
 // Per tile:  S = Q K^T (M = 128 rows, N = keys), P = exp2(S - m) by one thread per row, written
 // over S in tensor memory, O += P V with P as the tensor-memory operand.  Two softmax
@@ -25,8 +27,9 @@
 // moves only when a row's grows by more than 2^8, so O is rarely rescaled.
 //
 // P is rounded to bf16 for the product with V, which adds about as much error as rounding the
-// output to bf16; with an fp32 output the remainder p - bf16(p) takes a second product, so that
-// the output is good to about 2^-16.  Maxima, sums and O are fp32.
+// output to bf16; with an fp32 output, and in calls of at most 128 rows per sequence and KV head, the
+// remainder p - bf16(p) takes a second product, so that P is good to 2^-16.  Maxima, sums and O are
+// fp32.
 //
 // Warps: softmax; then one that issues the MMAs, one that walks the pieces and loads Q and K, one
 // that loads V (TMA boxes that never cross a page; two warps, because with 16-row pages one took
@@ -35,14 +38,14 @@
 // hold infinities or NaN.
 //
 // What bounds it, measured on a B200 (d = 128, 4 query heads per KV head): 1.1 to 1.2 PFLOP/s of
-// bf16 on prompt chunks (4 x 512 tokens at 32K: 917 us, 0.72 of the measured burst matrix rate;
-// an 8K prompt from nothing: 540 us).  A tile of two query tiles takes about 3,600 cycles for
+// bf16 on prompt chunks (4 x 512 tokens at 32K: 920-940 us, 0.71 of the measured burst matrix
+// rate; an 8K prompt from nothing: 540-570 us).  A tile of two query tiles takes about 3,600 cycles for
 // 2,048 of matrix work: a row's softmax (load of S, maximum, 128 exponentials, store of P: 2,300
 // cycles while the other warpgroup shares the pipes) and its products follow one another.  Tried
 // and slower: tiles of 64 keys with two S slots per stream (the N = 64 score MMAs take as long
 // as N = 128 ones: 1,427 us against 950), four softmax warpgroups on half tiles (1,430), S read
-// twice in chunks (1,277).  The products begin with the first half of P (about 1 %), an eighth of
-// the exponentials go to the FMA pipe (983 -> 950 us; a quarter 1,012, none 983).
+// twice in chunks (1,277).  The products begin with the first half of P (about 1 %); a few of the
+// exponentials go to the FMA pipe (none 983, an eighth or a sixteenth 950, a quarter 1,012 us).
 //
 // Every wait is bounded; on a timeout the kernel raises DEVFLAG_TIMEOUT, all roles leave their
 // loops, copies and MMAs in flight are drained, and tensor memory is freed.
@@ -61,7 +64,7 @@ namespace {
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kPaOCol = 256;   // first TMEM column of O; S (and P over it) below
 constexpr float kPaRescale = 8.f;   // log2 margin before the running maximum moves
-constexpr int kPaCubicEvery = 8;    // of so many pairs of exponentials, one goes to the FMA pipe
+constexpr int kPaCubicEvery = 16;    // of so many pairs of exponentials, one goes to the FMA pipe
 
 template <int D>
 struct Pa {
@@ -122,7 +125,8 @@ __device__ __forceinline__ uint64_t exp2_cubic2(uint64_t x) {
                __uint_as_float(__float_as_uint(b) + (__float_as_uint(nb) << 23)));
 }
 
-template <int D, bool F32>
+// F32: fp32 outputs; TWO: P in two bf16 parts.
+template <int D, bool F32, bool TWO>
 __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __grid_constant__ PaParams p) {
   using C = Pa<D>;
   constexpr int kTile = C::kTile, kWG = C::kWG, kDB = C::kDB, kNS = C::kStages;
@@ -137,6 +141,7 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const PagedAttnArgs& a = p.a;
 
+  asm volatile("griddepcontrol.launch_dependents;");  // the merge's blocks may come as CTAs leave
   if (tid == 0) {
     prefetch_tensormap(&p.q);
     prefetch_tensormap(&p.k);
@@ -198,11 +203,11 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
     if (lane == 0) mbar_arrive(&piece_empty[k % kPaPieces]);
   };
 
-  // Two softmax warpgroups at 208 registers and the other four warps at 88 make up the launch's 384 x 168
-  // (the split stands at the head of each branch, where the compiler can use it).
+  // Two softmax warpgroups at 200 registers and the other four warps at 104 make up the launch's 384 x 168
+  // (208 and 88: chunks 2 % slower; the split stands at the head of each branch, where the compiler can use it).
   if (warp < kMmaWarp) {
     // ------------------------------------------------------------------ softmax and output
-    if constexpr (kWG == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    if constexpr (kWG == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     const int wg = warp >> 2, quad = warp & 3;
     const int r = quad * 32 + lane, tr = r / p.G;
     const int rows_tile = p.tpt * p.G;
@@ -298,7 +303,7 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
           uint64_t l2[2] = {0, 0};
           // P over the scores it comes from: in the first 16 of 32 columns, its remainder in the other 16
           // (the cubic takes a masked score for 2^-126, which no fp32 sum notices; a row without keys is told by m)
-          constexpr bool kCubic = !F32 && kWG == 2;
+          constexpr bool kCubic = !TWO && kWG == 2;
 #pragma unroll
           for (int c = 0; c < kTile / 32; ++c) {
             uint32_t hi[16];
@@ -319,7 +324,7 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
               }
               l2[e & 1] = add2(l2[e & 1], pp);
               hi[e] = pack_bf16x2(p0, p1);
-              if constexpr (F32)
+              if constexpr (TWO)
                 lo[e] =
                     pack_bf16x2(p0 - bf16_bits_to_float(hi[e] & 0xFFFFu), p1 - __uint_as_float(hi[e] & 0xFFFF0000u));
             }
@@ -330,7 +335,7 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
               if (lane == 0) mbar_arrive(&p_half[slot]);
             }
             tmem_st16_nowait(s_col + 32 * c, hi);
-            if constexpr (F32) tmem_st16_nowait(s_col + 32 * c + 16, lo);
+            if constexpr (TWO) tmem_st16_nowait(s_col + 32 * c + 16, lo);
           }
           float la, lb;
           unpack2(add2(l2[0], l2[1]), la, lb);
@@ -409,7 +414,7 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
         }
       }
       tc_fence_before();
-      if (whole) {
+      if (whole || tall) {
         if (split_keys) ok = sync_wgs();  // neither accumulator is overwritten before both have read it
         release(piece);
         continue;
@@ -428,58 +433,11 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
       }
       ok = sync_wgs();
       if (!ok) break;
-      if (last_s && !tall) merge_pieces<C, F32>(p, s);
-      if (last_s && tall && active) {
-        // a thread per row and stream: two pieces' 32 columns under way at once
-        const int n = s.c_last - s.c_first + 1;
-        auto slot_of = [&](int k) { return 2 * (s.c_first + k) + (k == 0 ? 1 : 0); };
-        auto ml_of = [&](int k) { return __ldcg(a.part_ml + static_cast<int64_t>(slot_of(k)) * a.rows_cap + row); };
-        float M = -INFINITY, L = 0.f, z = 0.f, g = 0.f;
-        if (valid) {
-#pragma unroll 2
-          for (int k = 0; k < n; ++k) M = fmaxf(M, ml_of(k).x);
-          z = M == -INFINITY ? 0.f : M * p.scale_log2;
-#pragma unroll 2
-          for (int k = 0; k < n; ++k) {
-            const float2 ml = ml_of(k);
-            L = fmaf(exp2_approx(fmaf(ml.x, p.scale_log2, -z)), ml.y, L);
-          }
-          g = L > 0.f ? 1.f / L : 0.f;
-#pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            float acc[32];
-#pragma unroll
-            for (int e = 0; e < 32; ++e) acc[e] = 0.f;
-#pragma unroll 1
-            for (int k = 0; k < n; k += 2) {
-              const int k2 = min(k + 1, n - 1);
-              const float4* f0 = part_word(a, D, slot_of(k), 8 * c) + row;
-              const float4* f1 = part_word(a, D, slot_of(k2), 8 * c) + row;
-              float4 y0[8], y1[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                y0[e] = __ldcg(f0 + static_cast<int64_t>(e) * a.rows_cap);
-                y1[e] = __ldcg(f1 + static_cast<int64_t>(e) * a.rows_cap);
-              }
-              const float w0 = exp2_approx(fmaf(ml_of(k).x, p.scale_log2, -z)) * g;
-              const float w1 = k2 > k ? exp2_approx(fmaf(ml_of(k2).x, p.scale_log2, -z)) * g : 0.f;
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                acc[4 * e] = fmaf(w1, y1[e].x, fmaf(w0, y0[e].x, acc[4 * e]));
-                acc[4 * e + 1] = fmaf(w1, y1[e].y, fmaf(w0, y0[e].y, acc[4 * e + 1]));
-                acc[4 * e + 2] = fmaf(w1, y1[e].z, fmaf(w0, y0[e].z, acc[4 * e + 2]));
-                acc[4 * e + 3] = fmaf(w1, y1[e].w, fmaf(w0, y0[e].w, acc[4 * e + 3]));
-              }
-            }
-            store_out32<F32>(a.O, orow * D + 32 * c, acc);
-          }
-        }
-        if (valid && a.lse) a.lse[orow] = L > 0.f ? M * a.sm_scale + logf(L) : -INFINITY;
-      }
+      if (last_s) merge_pieces<C, F32>(p, s);
       release(piece);
     }
   } else {
-    if constexpr (kWG == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if constexpr (kWG == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     if (warp == kLoadWarp) {
       // ------------------------------------------------------------------ pieces, Q and K
       const int box = lane / kDB, db = lane % kDB;
@@ -493,6 +451,7 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
       // The rest of an item that an earlier CTA began comes last: the CTAs of a head then go through its
       // keys side by side, and find them in L2.
       bool late = false;
+      if (lane == 0) a.cuts[blockIdx.x].pieces = 0;
       for (int piece = 0; ok; ++piece) {
         const int at = piece % kPaPieces;
         if (piece >= kPaPieces) ok = all_ok(wait(&piece_empty[at], ((piece / kPaPieces) & 1) ^ 1));
@@ -510,6 +469,8 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
             c = late_piece;
           }
           if (lane == 0) {
+            if (c.t1 > 0 && c.t0 == 0 && c.t1 < c.it.ntiles && tall_item<C>(c.it, p.G))
+              a.cuts[blockIdx.x] = {c.q0, c.it.ntok * p.G, c.h, c.c_last - c.c_first + 1};
             pieces[at] = c;
             mbar_arrive(&piece_full[at]);
           }
@@ -651,7 +612,7 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
         auto values = [&](int slot, int o, uint32_t stage, bool first, int k0, int k1) {
           const uint32_t va = v_lo + stage * (C::kStageBytes >> 4);
 #pragma unroll
-          for (int part = 0; part < (F32 ? 2 : 1); ++part)
+          for (int part = 0; part < (TWO ? 2 : 1); ++part)
 #pragma unroll
             for (int kt = k0; kt < k1; ++kt)
               umma_bf16_ts_lo(tmem + kPaOCol + o * D,
@@ -766,17 +727,89 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
   }
 }
 
-// ------------------------------------------------------------------ host
+// Merges the cut items of many rows.  A block takes 32 rows and 32 columns of one; a thread takes one 16-byte word
+// of a row, four pieces' loads under way at once, in the order of the pieces.
 template <int D, bool F32>
+__global__ void __launch_bounds__(256, 5) paged_merge_kernel(PagedAttnArgs a, int G, float scale_log2) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the attention's launch is complete
+  const PagedCut cut = a.cuts[blockIdx.x];
+  const int row = blockIdx.y * 32 + (threadIdx.x & 31), word = blockIdx.z * 8 + (threadIdx.x >> 5);
+  if (cut.pieces == 0 || row >= cut.rows) return;
+  float M = -INFINITY, L = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int kParts = 4;
+  for (int k0 = 0; k0 < cut.pieces; k0 += kParts) {
+    float2 ml[kParts];
+    float4 v[kParts];
+#pragma unroll
+    for (int y = 0; y < kParts; ++y) {
+      ml[y] = make_float2(-INFINITY, 0.f);
+      v[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (k0 + y >= cut.pieces) continue;
+      // an item's first piece is the last of its CTA, the others the first of theirs
+      const int slot = 2 * (static_cast<int>(blockIdx.x) + k0 + y) + (k0 + y == 0 ? 1 : 0);
+      ml[y] = __ldcg(a.part_ml + static_cast<int64_t>(slot) * a.rows_cap + row);
+      v[y] = __ldcg(part_word(a, D, slot, word) + row);
+    }
+    float mn = M;
+#pragma unroll
+    for (int y = 0; y < kParts; ++y) mn = fmaxf(mn, ml[y].x);
+    const float z = mn == -INFINITY ? 0.f : mn * scale_log2;
+    const float w = exp2_approx(fmaf(M, scale_log2, -z));
+    M = mn;
+    L *= w;
+    o.x *= w, o.y *= w, o.z *= w, o.w *= w;
+#pragma unroll
+    for (int y = 0; y < kParts; ++y) {
+      const float u = exp2_approx(fmaf(ml[y].x, scale_log2, -z));
+      L = fmaf(u, ml[y].y, L);
+      o.x = fmaf(u, v[y].x, o.x), o.y = fmaf(u, v[y].y, o.y), o.z = fmaf(u, v[y].z, o.z), o.w = fmaf(u, v[y].w, o.w);
+    }
+  }
+  const float g = L > 0.f ? 1.f / L : 0.f;
+  const int64_t to = (cut.q0 + row / G) * a.Hq + cut.h * G + row % G;
+  if constexpr (F32)
+    reinterpret_cast<float4*>(static_cast<float*>(a.O) + to * D)[word] =
+        make_float4(o.x * g, o.y * g, o.z * g, o.w * g);
+  else
+    reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.O) + to * D)[word] =
+        make_uint2(pack_bf16x2(o.x * g, o.y * g), pack_bf16x2(o.z * g, o.w * g));
+  if (word == 0 && a.lse) a.lse[to] = L > 0.f ? M * a.sm_scale + logf(L) : -INFINITY;
+}
+
+// ------------------------------------------------------------------ host
+template <int D, bool F32, bool TWO>
 cudaError_t launch(const PagedAttnArgs& a, int num_sms, cudaStream_t s) {
   using C = Pa<D>;
   PaParams p;
   if (!paged_params<C>(a, paged_attn_tile_tokens(a.Hq / a.pool.Hkv), &p)) return cudaErrorInvalidValue;
-  auto kernel = paged_attn_kernel<D, F32>;
+  auto kernel = paged_attn_kernel<D, F32, TWO>;
   static int done[64] = {0};
   const cudaError_t e = set_smem_limit_once(kernel, C::kSmem, done);
   if (e != cudaSuccess) return e;
-  return launch_ex(kernel, dim3(num_sms), dim3(C::kThreads), C::kSmem, s, 0, p);
+  const cudaError_t e2 = launch_ex(kernel, dim3(num_sms), dim3(C::kThreads), C::kSmem, s, 0, p);
+  // rows that an item may have (tall_item)
+  const int64_t rows = static_cast<int64_t>(a.max_q_len) * p.G;
+  if (e2 != cudaSuccess || rows <= (C::kWG == 1 ? 32 : p.tpt * p.G)) return e2;
+  const dim3 blocks(num_sms, (a.rows_cap + 31) / 32, D / 32);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = blocks;
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_merge_kernel<D, F32>, a, p.G, p.scale_log2);
+}
+
+// At most 128 rows per sequence and KV head: bound by memory, and too few for the roundings of P to average out.
+template <int D>
+cudaError_t launch(const PagedAttnArgs& a, int num_sms, cudaStream_t s) {
+  const bool two = static_cast<int64_t>(a.max_q_len) * (a.Hq / a.pool.Hkv) <= 128;
+  if (!a.out_bf16) return launch<D, true, true>(a, num_sms, s);
+  return two ? launch<D, false, true>(a, num_sms, s) : launch<D, false, false>(a, num_sms, s);
 }
 
 }  // namespace
@@ -790,9 +823,9 @@ int paged_attn_rows(int d, int G, int64_t max_q_len) {
 
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, int num_sms, cudaStream_t s) {
   switch (a.pool.d) {
-    case 64: return a.out_bf16 ? launch<64, false>(a, num_sms, s) : launch<64, true>(a, num_sms, s);
-    case 128: return a.out_bf16 ? launch<128, false>(a, num_sms, s) : launch<128, true>(a, num_sms, s);
-    case 256: return a.out_bf16 ? launch<256, false>(a, num_sms, s) : launch<256, true>(a, num_sms, s);
+    case 64: return launch<64>(a, num_sms, s);
+    case 128: return launch<128>(a, num_sms, s);
+    case 256: return launch<256>(a, num_sms, s);
   }
   return cudaErrorNotSupported;
 }

@@ -59,8 +59,8 @@ __device__ __forceinline__ Item item_at(const PaParams& p, int nq, int len, int 
   return it;
 }
 
-// Items of more than a warp's rows, each row whole in one accumulator, are merged by a thread per row; the
-// others word by word.
+// Cut items of more than a warp's rows, each row whole in one accumulator, are merged by a launch of their own
+// over the whole GPU; the others by the CTA that finishes them last.
 template <class C>
 __device__ __forceinline__ bool tall_item(const Item& it, int G) {
   return (!it.solo || C::kWG == 1) && it.ntok * G > 32;
@@ -180,7 +180,7 @@ __device__ __forceinline__ void line_lengths(const PaParams& p, int64_t* seq_uni
       const Item it = item_at<C>(p, t.nq, t.len, j);
       const int64_t u = item_units<C>(it);
       n += u;
-      const float cost = tall_item<C>(it, p.G) ? C::kD / 64 : it.ntok * p.G * (C::kD / 8192.f);
+      const float cost = tall_item<C>(it, p.G) ? 0.15f : it.ntok * p.G * (C::kD / 8192.f);
       merge = fmaxf(merge, u * cost);
     }
     if (wide) {
