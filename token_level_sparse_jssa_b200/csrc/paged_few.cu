@@ -10,7 +10,7 @@
 //
 // Measured on a B200: one token over 4 x 100K-131K rows of 8 heads, d = 128, 295 us, the rate of a plain
 // copy; with the 128-row tiles 303, and 333 under sustained load.  One token of a 2K sequence 14.5 us
-// (16.7), of 64 sequences of 700-3,000 tokens 91 us (105), of 16 with d = 64 47 us (62).  Two query rows
+// (16.7), of 64 sequences of 700-3,000 tokens 93 us (105), of 16 with d = 64 49 us (62).  Two query rows
 // over 8 windows of 1,024 keys, d = 256: 28 us, of which 5 until the first keys arrive, 11 for 67 MB of
 // keys and values, and 10 to add up the warps and merge the pieces.
 //
