@@ -105,9 +105,12 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// 2^x of two values on the FMA pipe, for -126 <= x < 127 (lower ones count as -126): x = n + f with
-// n the nearest integer, read off the low bits of x + 1.5 2^23, and 2^f on [-1/2, 1/2] by the
-// cubic of least maximal relative error (7.5e-5, found by exchange; p is rounded to bf16, 3.9e-3).
+// 2^x of two values on the FMA pipe, for x < 127: x = n + f with n the nearest integer, read off the low
+// bits of x + 1.5 2^23, and 2^f on [-1/2, 1/2] by the cubic of least maximal relative error (7.5e-5, found by
+// exchange; p is rounded to bf16, 3.9e-3).  What x = -126 and everything below it gives, kExp2Least, is taken off at the
+// end: a masked key's weight has to be 0, because the value that it would bring along may be as large as bf16 goes.
+constexpr float kCubic0 = 0.999928057f;
+constexpr uint32_t kExp2Least = 0x007FFB49u;  // the bits of kCubic0, 126 off its exponent
 __device__ __forceinline__ uint64_t exp2_cubic2(uint64_t x) {
   float a, b, na, nb;
   unpack2(x, a, b);
@@ -118,11 +121,13 @@ __device__ __forceinline__ uint64_t exp2_cubic2(uint64_t x) {
   const uint64_t f = fma2(n, pack2(-1.f, -1.f), x);
   uint64_t y = fma2(f, pack2(0.0551716685f, 0.0551716685f), pack2(0.242611125f, 0.242611125f));
   y = fma2(y, f, pack2(0.693260968f, 0.693260968f));
-  y = fma2(y, f, pack2(0.999928057f, 0.999928057f));
+  y = fma2(y, f, pack2(kCubic0, kCubic0));
   unpack2(y, a, b);
   unpack2(t, na, nb);
-  return pack2(__uint_as_float(__float_as_uint(a) + (__float_as_uint(na) << 23)),
-               __uint_as_float(__float_as_uint(b) + (__float_as_uint(nb) << 23)));
+  const float least = __uint_as_float(kExp2Least | 0x80000000u);
+  return add2(pack2(__uint_as_float(__float_as_uint(a) + (__float_as_uint(na) << 23)),
+                    __uint_as_float(__float_as_uint(b) + (__float_as_uint(nb) << 23))),
+              pack2(least, least));
 }
 
 // F32: fp32 outputs; TWO: P in two bf16 parts.
@@ -302,7 +307,6 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
           const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2), mm2 = pack2(-mm, -mm);
           uint64_t l2[2] = {0, 0};
           // P over the scores it comes from: in the first 16 of 32 columns, its remainder in the other 16
-          // (the cubic takes a masked score for 2^-126, which no fp32 sum notices; a row without keys is told by m)
           constexpr bool kCubic = !TWO && kWG == 2;
 #pragma unroll
           for (int c = 0; c < kTile / 32; ++c) {
