@@ -10,7 +10,7 @@ import pytest
 import torch
 
 import token_level_sparse_jssa_b200 as jssa
-from tests._paged import seen_mask
+from tests._paged import attention64, seen_mask
 from tests.test_gpu_paged import Problem
 
 pytestmark = pytest.mark.gpu
@@ -18,9 +18,95 @@ pytestmark = pytest.mark.gpu
 BOTH = pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
 
 
+def _fill(p, pool, b, rows):
+    """Writes rows [T, Hkv, d] as sequence b's seen tokens p.t[b] into a pool."""
+    t = p.t[b]
+    if len(t):
+        pool[p.table[b].long()[t // p.page], :, t % p.page] = rows.to(torch.bfloat16)
+
+
 def _seen(p, b):
     """[queries, seen tokens] of sequence b, as a mask."""
     return seen_mask(p.pos[b], p.t[b], p.window, p.sinks)
+
+
+# --------------------------------------------------------------------------- probabilities
+def _two_level(p):
+    """Every 16th token has logit 0 and the others log(0.50193), which lies between two bf16 values (0.5 is 3.9e-3 off), so
+    that each key warp and tile keeps its maximum at 0; the values cancel, so that the
+    output is small beside sum p|v| and its own rounding hides nothing."""
+    p.scale = 1.0
+    p.Q.zero_()
+    p.Q[..., 0] = 1.0
+    for b in range(len(p.lens)):
+        top = (p.t[b] % 16 == 0)
+        k = torch.zeros(len(p.t[b]), p.Hkv, p.d, device="cuda")
+        k[:, :, 0] = torch.where(top, 0.0, -1.0)[:, None]
+        v = torch.where(top, -7.53125, 1.0)[:, None, None].expand_as(k)
+        _fill(p, p.K, b, k)
+        _fill(p, p.V, b, v)
+        p.k64[b], p.v64[b] = (x.to(torch.bfloat16).transpose(0, 1) for x in (k, v))
+    p.scale = 0.68929454   # -log(0.50193)
+
+
+def _check_two_level(p, two):
+    torch.cuda.synchronize()
+    assert jssa.read_device_status(p.ws)[1] == 0
+    for b in range(len(p.lens)):
+        lo, hi = p.begin[b], p.begin[b + 1]
+        if lo == hi:
+            continue
+        want, a, _ = attention64(p.Q[lo:hi], p.k64[b], p.v64[b], p.pos[b], p.t[b], p.window, p.sinks, p.scale)
+        # p: two parts 2^-16, the exponential, the logit's and the scale's rounding 2^-20; sums of at most
+        # lens[b] terms in fp32, above and below the line.  One part: 2^-8 in place of 2^-16, and 7.5e-5 of the cubic.
+        tol = (2.0 ** -16 if two(b) else 2.0 ** -8 + 2.0 ** -13) + 2.0 ** -20 + 2 * p.lens[b] * 2.0 ** -24
+        tol = tol * a + (2.0 ** -8 if p.out == torch.bfloat16 else 2.0 ** -24) * want.abs()
+        err = (p.O[lo:hi].double() - want).abs()
+        assert bool((err <= tol).all()), (b, float((err / a).max()))
+
+
+@BOTH
+@pytest.mark.parametrize("kw", [
+    dict(lens=[600, 31], nq=[1, 1], G=4), dict(lens=[600, 17], nq=[4, 3], d=64, G=8, Hkv=1),
+    dict(lens=[500], nq=[2], d=256, G=4, page=64), dict(lens=[700, 90], nq=[30, 5], G=4, window=300, sinks=5),
+    dict(lens=[700, 90], nq=[16, 1], G=8, d=64), dict(lens=[700, 90], nq=[64, 9], G=2, d=256),
+    dict(lens=[300], nq=[1], G=128, Hkv=1),
+])
+def test_few_rows_keep_sixteen_bits_of_a_probability(kw, out):
+    p = Problem(**kw, out=out)
+    _two_level(p)
+    p.run()
+    _check_two_level(p, lambda b: True)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_fp32_outputs_keep_sixteen_bits_of_a_probability(d):
+    p = Problem([700, 90, 300], [300, 1, 5], d=d, G=4, out=torch.float32)
+    _two_level(p)
+    p.run()
+    _check_two_level(p, lambda b: True)
+
+
+@pytest.mark.parametrize("window", [0, 300])
+@pytest.mark.parametrize("d,G", [(64, 4), (128, 4), (256, 2), (128, 16), (64, 128)])
+def test_precision_is_a_sequences_own(d, G, window):
+    # sequences of at most 128 rows per KV head beside a prompt chunk, and under a generous bound
+    few = 128 // G
+    p = Problem([700, 600, 450, 90, 500], [200, 1, few, min(3, few), few + 1], d=d, Hkv=1, G=G, window=window, sinks=3)
+    _two_level(p)
+    p.run()
+    _check_two_level(p, lambda b: b in (1, 2, 3))
+    p = Problem([600, 90], [1, few], d=d, Hkv=1, G=G, window=window, sinks=3)
+    p.max_q = 5000
+    p.ws = jssa.alloc_paged_workspace(p.L, p.max_q)
+    _two_level(p)
+    p.run()
+    _check_two_level(p, lambda b: True)
+    if G == 4:   # cut over the whole GPU
+        p = Problem([700, 9000], [200, 1], d=d, Hkv=1, G=G, window=0)
+        _two_level(p)
+        p.run()
+        _check_two_level(p, lambda b: b == 1)
 
 
 # --------------------------------------------------------------------------- hidden rows

@@ -26,10 +26,11 @@
 // two halves are added at the end.  O stays in tensor memory; the maximum that P refers to
 // moves only when a row's grows by more than 2^8, so O is rarely rescaled.
 //
-// P is rounded to bf16 for the product with V, which adds about as much error as rounding the
-// output to bf16; with an fp32 output, and in calls of at most 128 rows per sequence and KV head, the
-// remainder p - bf16(p) takes a second product, so that P is good to 2^-16.  Maxima, sums and O are
-// fp32.
+// P goes into the product with V in two bf16 parts, bf16(p) and p - bf16(p), so that it is good to 2^-16:
+// with an fp32 output, and for every sequence whose new tokens fit one query tile (at most 128 rows per KV head), whatever
+// else is in the call.  Longer ones with a bf16 output have it rounded to bf16, which adds about as much error as
+// rounding the output does, and one exponential in 16 from a cubic good to 7.5e-5 (in the sums and in lse too).
+// Maxima, sums and O are fp32.
 //
 // Warps: softmax; then one that issues the MMAs, one that walks the pieces and loads Q and K, one
 // that loads V (TMA boxes that never cross a page; two warps, because with 16-row pages one took
@@ -130,7 +131,7 @@ __device__ __forceinline__ uint64_t exp2_cubic2(uint64_t x) {
               pack2(least, least));
 }
 
-// F32: fp32 outputs; TWO: P in two bf16 parts.
+// F32: fp32 outputs; TWO: P in two bf16 parts in every item, else in those that hold all of a sequence's new tokens.
 template <int D, bool F32, bool TWO>
 __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __grid_constant__ PaParams p) {
   using C = Pa<D>;
@@ -230,6 +231,7 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
       const Piece& s = take(piece, &ok);
       if (!ok) break;
       const bool solo = s.it.solo;
+      [[maybe_unused]] const bool few = s.it.few;
       const int qoff = !solo && wg == 1 ? p.tpt : 0;
       const bool valid = r < rows_tile && qoff + tr < s.it.ntok;
       const bool active = __any_sync(0xFFFFFFFFu, valid);
@@ -258,18 +260,20 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
           float x[kTile];
           if constexpr (kTile == 128) tmem_ld128(s_col, x);
           else tmem_ld64(s_col, x);
+          // 32 scores from column 32 c on, those that this row does not see at -infinity
+          auto hide = [&](int c, float* y) {
+            const int at = v0 + 32 * c;
+            uint32_t w = bits_below(va - at) | (bits_below(vc - at) & ~bits_below(vb - at));
+            if (bad)
+              for (int k = 0; k < p.nbox; ++k)
+                if ((bad >> (k * kDB)) & 1)
+                  w &= ~(bits_below((k + 1) * p.box - 32 * c) & ~bits_below(k * p.box - 32 * c));
+#pragma unroll
+            for (int e = 0; e < 32; ++e) y[e] = (w >> e) & 1 ? y[e] : -INFINITY;
+          };
           if (masked) {
 #pragma unroll
-            for (int c = 0; c < kTile / 32; ++c) {
-              const int at = v0 + 32 * c;
-              uint32_t w = bits_below(va - at) | (bits_below(vc - at) & ~bits_below(vb - at));
-              if (bad)
-                for (int k = 0; k < p.nbox; ++k)
-                  if ((bad >> (k * kDB)) & 1)
-                    w &= ~(bits_below((k + 1) * p.box - 32 * c) & ~bits_below(k * p.box - 32 * c));
-#pragma unroll
-              for (int e = 0; e < 32; ++e) x[32 * c + e] = (w >> e) & 1 ? x[32 * c + e] : -INFINITY;
-            }
+            for (int c = 0; c < kTile / 32; ++c) hide(c, x + 32 * c);
           }
           float m4[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
@@ -306,15 +310,14 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
           const float mm = m == -INFINITY ? 0.f : m * p.scale_log2;
           const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2), mm2 = pack2(-mm, -mm);
           uint64_t l2[2] = {0, 0};
-          // P over the scores it comes from: in the first 16 of 32 columns, its remainder in the other 16
-          constexpr bool kCubic = !TWO && kWG == 2;
-#pragma unroll
-          for (int c = 0; c < kTile / 32; ++c) {
+          // P of 32 scores over the columns they come from: in the first 16, its remainder in the other 16
+          auto weigh = [&](int c, const float* y, auto two_parts) {
+            constexpr bool kTwo = decltype(two_parts)::value, kCubic = !kTwo && kWG == 2;
             uint32_t hi[16];
             [[maybe_unused]] uint32_t lo[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const uint64_t z = fma2(pack2(x[32 * c + 2 * e], x[32 * c + 2 * e + 1]), scale2, mm2);
+              const uint64_t z = fma2(pack2(y[2 * e], y[2 * e + 1]), scale2, mm2);
               float p0, p1;
               uint64_t pp;
               if (kCubic && e % kPaCubicEvery == kPaCubicEvery - 1) {
@@ -328,7 +331,7 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
               }
               l2[e & 1] = add2(l2[e & 1], pp);
               hi[e] = pack_bf16x2(p0, p1);
-              if constexpr (TWO)
+              if constexpr (kTwo)
                 lo[e] =
                     pack_bf16x2(p0 - bf16_bits_to_float(hi[e] & 0xFFFFu), p1 - __uint_as_float(hi[e] & 0xFFFF0000u));
             }
@@ -339,7 +342,19 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
               if (lane == 0) mbar_arrive(&p_half[slot]);
             }
             tmem_st16_nowait(s_col + 32 * c, hi);
-            if constexpr (TWO) tmem_st16_nowait(s_col + 32 * c + 16, lo);
+            if constexpr (kTwo) tmem_st16_nowait(s_col + 32 * c + 16, lo);
+          };
+          if (!TWO && few) {  // rare beside prompts: the scores are read again, so that the other way keeps its registers
+#pragma unroll 1
+            for (int c = 0; c < kTile / 32; ++c) {
+              float y[32];
+              tmem_ld32(s_col + 32 * c, y);
+              if (masked) hide(c, y);
+              weigh(c, y, std::true_type{});
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < kTile / 32; ++c) weigh(c, x + 32 * c, std::bool_constant<TWO>{});
           }
           float la, lb;
           unpack2(add2(l2[0], l2[1]), la, lb);
@@ -613,15 +628,18 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
             umma_bf16_lo(tmem + slot * C::kSCols, qa + (kk >> 2) * (C::kQBlock >> 4) + (kk & 3) * 2,
                          ka + (kk >> 2) * (kTile * 128 >> 4) + (kk & 3) * 2, idesc_s, kk != 0);
         };
-        auto values = [&](int slot, int o, uint32_t stage, bool first, int k0, int k1) {
+        // the steps k0 <= kt < k1 of the product of one part of P with V
+        auto product = [&](int slot, int o, uint32_t stage, bool first, int k0, int k1, int part) {
           const uint32_t va = v_lo + stage * (C::kStageBytes >> 4);
 #pragma unroll
-          for (int part = 0; part < (TWO ? 2 : 1); ++part)
-#pragma unroll
-            for (int kt = k0; kt < k1; ++kt)
-              umma_bf16_ts_lo(tmem + kPaOCol + o * D,
-                              tmem + slot * C::kSCols + (kt >> 1) * 32 + part * 16 + (kt & 1) * 8,
-                              va + kt * (2048 >> 4) + (kt >> box_shift) * box_skip, idesc_o, part || kt ? 1u : !first);
+          for (int kt = k0; kt < k1; ++kt)
+            umma_bf16_ts_lo(tmem + kPaOCol + o * D,
+                            tmem + slot * C::kSCols + (kt >> 1) * 32 + part * 16 + (kt & 1) * 8,
+                            va + kt * (2048 >> 4) + (kt >> box_shift) * box_skip, idesc_o, part || kt ? 1u : !first);
+        };
+        auto values = [&](int slot, int o, uint32_t stage, bool first, int k0, int k1) {
+          product(slot, o, stage, first, k0, k1, 0);
+          if constexpr (TWO) product(slot, o, stage, first, k0, k1, 1);
         };
         for (int piece = 0; ok; ++piece) {
           const int at = piece % kPaPieces;
@@ -629,6 +647,7 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
           if (!ok || pieces[at].t1 == 0) break;
           const int n = pieces[at].t1 - pieces[at].t0;
           const bool pair = !pieces[at].it.solo;
+          [[maybe_unused]] const bool few = pieces[at].it.few;
           mbar_arrive(&piece_empty[at]);
           ok = wait(&q_full, piece & 1) && wait(&kv_full[ks], k_par);
           if (!ok) break;
@@ -702,6 +721,8 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
               p_par ^= 1u << slot;
               tc_fence_after();
               values(slot, o, vs, i == 0 || (kWG == 2 && i == 1), 0, kTile / 16);
+              if constexpr (!TWO)
+                if (few) product(slot, o, vs, false, 0, kTile / 16, 1);
               umma_commit(&kv_empty[vs]);
               if (kWG == 1 || !more) umma_commit(&o_full[slot]);
               next_v();
@@ -808,7 +829,9 @@ cudaError_t launch(const PagedAttnArgs& a, int num_sms, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, paged_merge_kernel<D, F32>, a, p.G, p.scale_log2);
 }
 
-// At most 128 rows per sequence and KV head: bound by memory, and too few for the roundings of P to average out.
+// Where no sequence can have more than 128 rows per KV head, a kernel of its own has nothing but the two-part form: 8
+// tokens of 8-head groups over 16 caches of 12K, d = 64: 47.5 us, 52.4 in the one that has both; of 4-head groups over 8
+// caches of 5K, d = 128: 53.2 and 55.1.  P, and so the result's precision, is the same in either.
 template <int D>
 cudaError_t launch(const PagedAttnArgs& a, int num_sms, cudaStream_t s) {
   const bool two = static_cast<int64_t>(a.max_q_len) * (a.Hq / a.pool.Hkv) <= 128;

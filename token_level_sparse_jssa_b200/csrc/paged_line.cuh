@@ -32,6 +32,7 @@ struct Item {
   int tok0, ntok, pf;
   int s_al, shift, z0, z1, nv, ntiles;
   bool solo;  // one query tile
+  bool few;   // and all of its sequence's new tokens
 };
 
 template <class C>
@@ -56,6 +57,7 @@ __device__ __forceinline__ Item item_at(const PaParams& p, int nq, int len, int 
   it.nv = hi - it.shift;
   it.ntiles = (it.nv + C::kTile - 1) / C::kTile;
   it.solo = C::kWG == 1 || it.ntok <= p.tpt;
+  it.few = nq <= p.tpt;
   return it;
 }
 
