@@ -11,7 +11,7 @@ import torch
 
 import token_level_sparse_jssa_b200 as jssa
 from tests._paged import attention64, seen_mask
-from tests.test_gpu_paged import Problem
+from tests.test_gpu_paged import CASES, Problem
 
 pytestmark = pytest.mark.gpu
 
@@ -28,6 +28,79 @@ def _fill(p, pool, b, rows):
 def _seen(p, b):
     """[queries, seen tokens] of sequence b, as a mask."""
     return seen_mask(p.pos[b], p.t[b], p.window, p.sinks)
+
+
+# --------------------------------------------------------------------------- which rows are seen
+@BOTH
+@pytest.mark.parametrize("kw", CASES)
+def test_every_seen_row_counts_once(kw, out):
+    # Equal logits (Q = 0): every p is 1, the output is the mean of the seen rows and lse = log n.  V holds whole numbers
+    # from -127 to 127 but 0, whose sums are exact in fp32 (at most 16,000 rows: under 2^21), so in fp32 the
+    # output is off by the reciprocal's and the product's rounding, and a lost or doubled row moves it by more:
+    # by 1/n at least, against 2^-23 |mean| with |mean| <= 127 and n <= 16,000.  In bf16, 2^-8 of the rounding, 2^-15
+    # of the row sum's exponentials (7.5e-5 on one in 16), and the row test below tells single rows.
+    p = Problem(**kw, out=out)
+    p.Q.zero_()
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    v = []
+    for b in range(len(p.lens)):
+        x = torch.randint(1, 128, (len(p.t[b]), p.Hkv, p.d), generator=g, device="cuda")
+        x *= 1 - 2 * torch.randint(0, 2, x.shape, generator=g, device="cuda")
+        _fill(p, p.V, b, x)
+        v.append(x.double())
+    p.run()
+    torch.cuda.synchronize()
+    assert jssa.read_device_status(p.ws)[1] == 0
+    tol, lse_tol = (2.0 ** -22.9, 2.0 ** -21) if out == torch.float32 else (2.0 ** -8 + 2.0 ** -15, 2.0 ** -15)
+    for b in range(len(p.lens)):
+        lo, hi = p.begin[b], p.begin[b + 1]
+        if lo == hi:
+            continue
+        m = _seen(p, b).double()
+        n = m.sum(1)
+        want = torch.einsum("qt,thd->qhd", m, v[b]) / n[:, None, None]
+        want = want.repeat_interleave(p.Hq // p.Hkv, 1)
+        err = (p.O[lo:hi].double() - want).abs()
+        assert bool((err <= tol * want.abs()).all()), (b, float((err / want.abs().clamp(min=1e-30)).max()))
+        lse = n.log()[:, None]
+        assert bool(((p.lse[lo:hi].double() - lse).abs() <= lse_tol * (1 + lse)).all()), b
+
+
+@BOTH
+@pytest.mark.parametrize("kw", CASES)
+def test_each_edge_row_is_seen_by_its_queries_alone(kw, out):
+    # Column e of V is 64 in one row alone, in turn at the ends of pages, tiles, windows, sinks and sequences: the output's
+    # column is 64 / n for the queries that see that row and exactly 0 for the others.
+    p = Problem(**kw, out=out)
+    p.Q.zero_()
+    rows = []
+    for b in range(len(p.lens)):
+        t = p.t[b]
+        edge = {0, 1, p.lens[b] - 1, p.lens[b] - p.nq[b], p.lens[b] - p.nq[b] - 1, p.sinks - 1, p.sinks}
+        for q in (p.lens[b] - p.nq[b], p.lens[b] - 1):
+            edge |= {q - p.window, q - p.window + 1, q - p.window + 2}
+        for unit in (p.page, 64, 128):
+            for x in (p.lens[b] // 2, p.lens[b] - p.nq[b], p.lens[b] - 1):
+                edge |= {x // unit * unit - 1, x // unit * unit}
+        at = [i for i, x in enumerate(t.tolist()) if x in edge]
+        at = (at * p.d)[:p.d] if len(at) < p.d else at[:p.d]
+        x = torch.zeros(len(t), p.Hkv, p.d, device="cuda")
+        if at:
+            x[torch.tensor(at), :, torch.arange(p.d)] = 64.0
+        _fill(p, p.V, b, x)
+        rows.append(at)
+    p.run()
+    torch.cuda.synchronize()
+    assert jssa.read_device_status(p.ws)[1] == 0
+    tol = 2.0 ** -22.9 if out == torch.float32 else 2.0 ** -8 + 2.0 ** -15
+    for b in range(len(p.lens)):
+        lo, hi = p.begin[b], p.begin[b + 1]
+        if lo == hi:
+            continue
+        m = _seen(p, b).double()
+        want = (64.0 * m[:, rows[b]] / m.sum(1, keepdim=True))[:, None, :]
+        assert bool(((p.O[lo:hi].double() - want).abs() <= tol * want).all()), b
 
 
 # --------------------------------------------------------------------------- probabilities
