@@ -329,7 +329,10 @@ JSSA_API jssa_status jssa_calibrate(const jssa_layout* L, const void* Qc, const 
  *   page_table  device int32 [B, max_pages], contiguous: token t of sequence b is row
  *               t % page_size of page page_table[b, t / page_size]; -1 marks an entry without a page
  *   ref_count   device int32 [n_pages]: table entries that name the page (0: free)
- *   seq_lens    device int32 [B]: tokens in the cache, at most max_pages * page_size
+ *   seq_lens    device int32 [B]: tokens in the cache, at most max_pages * page_size.  Between calls a length
+ *               may be lowered (tokens taken back) to one whose last page is still in the table: entries
+ *               past the length keep their pages until fork or reserve writes over them, which gives
+ *               the pages up first, or release ends the sequence
  * Q heads as elsewhere: query head hq belongs to KV head hq / G, G = Hq / Hkv.
  * Supported: d in {64, 128, 256}, 1 <= G <= 128, page_size a multiple of 16, B <= 1024,
  * max_pages * page_size <= 2^30, a page of a pool below 2^33 elements.  Pool pointers 16-byte

@@ -58,6 +58,19 @@ __device__ __forceinline__ int clamp_len(int len, const PageBook& k, bool* bad) 
   return len < 0 ? 0 : (len > cap ? static_cast<int>(cap) : len);
 }
 
+// A table entry past its sequence's length (a sequence that gave tokens back) still counts as a holder of its page;
+// before fork or reserve writes over it, the page is given up.  A page that is counted free already keeps its count, and
+// the entry, which cannot be right, is cleared.
+__device__ __forceinline__ void give_up(const PageBook& k, int32_t* entry) {
+  const int p = *entry;
+  if (p < 0 || p >= k.n_pages) return;
+  if (atomicSub(k.ref + p, 1) <= 0) {
+    atomicAdd(k.ref + p, 1);
+    *entry = -1;
+    flag_error(k.status, DEVFLAG_BAD_INDEX);
+  }
+}
+
 // ------------------------------------------------------------------ fork
 // One block per entry: validates it against the whole list, then copies the table row and
 // counts its pages.  Rows that are forked to are neither read nor written by other entries.
@@ -90,6 +103,7 @@ __global__ void __launch_bounds__(256) pages_fork_kernel(PageBook k, const int32
       p = -1;
     }
     if (p >= 0) atomicAdd(k.ref + p, 1);
+    give_up(k, to + j);
     to[j] = p < 0 ? -1 : p;
   }
   if (bad_page) flag_error(k.status, DEVFLAG_BAD_INDEX);
@@ -104,6 +118,9 @@ __global__ void __launch_bounds__(256) pages_fork_kernel(PageBook k, const int32
 // and m growers is given up by every grower but, when m = r, the last one (sequence by
 // sequence, each that leaves lowers the count, and the last finds itself alone): m and the
 // highest grower come from two atomics per page in `growers`, cleared before them.
+// Entries that will be written are given up first (by their sequence's thread where they are one or two, by a warp
+// otherwise), so that pages that a sequence holds past its length serve it again; when the call
+// fails they are taken back.
 // The free pages are listed in ascending order until enough are found: a pass takes 16 x 1024
 // counts, a ballot per 32 of them, and one scan over the 512 ballots ranks them all.  The first
 // 4096 stay in shared memory.  Then a warp per sequence writes the entries.
@@ -112,9 +129,10 @@ __global__ void __launch_bounds__(1024) pages_reserve_kernel(PageBook k, const i
                                                              int32_t* copy_dst, int32_t* growers, int32_t* free_list) {
   __shared__ int part[33];
   __shared__ int lo_s[1024], cnt_s[1024], off_s[1024], votes_s[kReservePer * 32], near_s[kReserveNear];
-  const int b = threadIdx.x;
+  __shared__ int past_s[1024], many_s[1024];
+  const int b = threadIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int ps = k.page_size;
-  int len = 0, add = 0, last = -1;
+  int len = 0, add = 0, last = -1, past = 0, n_past = 0;  // entries from the length's end on that will be written
   bool fail = false, part_page = false;
   if (b < k.B) {
     bool bad;
@@ -125,6 +143,12 @@ __global__ void __launch_bounds__(1024) pages_reserve_kernel(PageBook k, const i
       add = 0;
     }
     if (static_cast<int64_t>(len) + add > static_cast<int64_t>(k.max_pages) * ps) fail = true;
+    if (add > 0 && !fail) {
+      past = static_cast<int>(ceil_div(len, ps));
+      n_past = static_cast<int>(ceil_div(static_cast<int64_t>(len) + add, ps)) - past;
+    }
+    past_s[b] = past;
+    many_s[b] = n_past > 2 ? n_past : 0;
     part_page = add > 0 && len % ps != 0;
     if (part_page) {
       last = k.table[static_cast<int64_t>(b) * k.max_pages + len / ps];
@@ -138,8 +162,15 @@ __global__ void __launch_bounds__(1024) pages_reserve_kernel(PageBook k, const i
     growers[2 * static_cast<int64_t>(last)] = 0;
     growers[2 * static_cast<int64_t>(last) + 1] = 0;
   }
+  auto past_entries = [&](auto each) {
+    if (n_past <= 2)
+      for (int j = 0; j < n_past; ++j) each(k.table + static_cast<int64_t>(b) * k.max_pages + past + j);
+    for (int q = warp; q < k.B; q += 32)
+      for (int j = lane; j < many_s[q]; j += 32) each(k.table + static_cast<int64_t>(q) * k.max_pages + past_s[q] + j);
+  };
   __threadfence_block();
   fail = __syncthreads_or(fail) != 0;
+  if (!fail) past_entries([&](int32_t* e) { give_up(k, e); });
   if (!fail && part_page) {
     atomicAdd(growers + 2 * static_cast<int64_t>(last), 1);
     atomicMax(growers + 2 * static_cast<int64_t>(last) + 1, b + 1);
@@ -148,7 +179,7 @@ __global__ void __launch_bounds__(1024) pages_reserve_kernel(PageBook k, const i
   __syncthreads();
   bool split = false;
   if (!fail && part_page) {
-    const int r = k.ref[last];
+    const int r = __ldcg(k.ref + last);
     const int m = __ldcg(growers + 2 * static_cast<int64_t>(last));
     const int top = __ldcg(growers + 2 * static_cast<int64_t>(last) + 1);
     split = r > 1 && (m < r || top != b + 1);
@@ -164,7 +195,6 @@ __global__ void __launch_bounds__(1024) pages_reserve_kernel(PageBook k, const i
   cnt_s[b] = cnt;
   off_s[b] = off;
   int found = 0;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int64_t base = 0; !fail && base < k.n_pages && found < total; base += 1024 * kReservePer) {
     uint32_t votes[kReservePer];
     int ref[kReservePer];
@@ -196,7 +226,12 @@ __global__ void __launch_bounds__(1024) pages_reserve_kernel(PageBook k, const i
     __syncthreads();
   }
   auto nth_free = [&](int rank) { return rank < kReserveNear ? near_s[rank] : __ldcg(free_list + rank); };
-  if (found < total) fail = true;
+  if (!fail && found < total) {
+    past_entries([&](int32_t* e) {
+      if (*e >= 0 && *e < k.n_pages) atomicAdd(k.ref + *e, 1);
+    });
+    fail = true;
+  }
   if (fail) {
     if (b < k.B) copy_src[b] = copy_dst[b] = -1;
     if (b == 0) flag_error(k.status, DEVFLAG_NO_PAGES);
