@@ -355,7 +355,8 @@ JSSA_API jssa_status jssa_calibrate(const jssa_layout* L, const void* Qc, const 
  * Checks on the device: a sequence whose length is outside [0, max_pages * page_size], or whose
  * rows in q_begin are out of order, past n_tokens or more than its length, raises
  * JSSA_DEV_BAD_SEQ_LEN and is left out (append and attention write none of its rows; the page
- * calls clamp the length).  A page-table entry that a call needs and that is no page raises
+ * calls clamp the length).  A call with n_tokens = 0 (or max_q_len = 0) returns at once: it reads,
+ * checks and writes nothing.  A page-table entry that a call needs and that is no page raises
  * JSSA_DEV_BAD_INDEX (its tokens are not written; attention leaves them out).
  */
 typedef struct {

@@ -435,10 +435,17 @@ __device__ __forceinline__ int append_place(const PagedAppendArgs& a, int64_t i,
 }
 
 // A block takes kAppendTokens tokens: their places first, then their vectors, four loads of a
-// thread under way before its first store.
+// thread under way before its first store.  The last block has none: it looks at every sequence, because one in
+// disorder may have no token that would come upon it.
 constexpr int kAppendTokens = 8, kAppendPer = 4;
 __global__ void __launch_bounds__(256) paged_append_kernel(PagedAppendArgs a) {
   __shared__ int page_s[kAppendTokens], row_s[kAppendTokens];
+  if (blockIdx.x == gridDim.x - 1) {
+    for (int b = threadIdx.x; b < a.B; b += blockDim.x)
+      new_tokens(a.q_begin, a.seq_lens, b, static_cast<int64_t>(a.max_pages) * a.pool.page_size, a.n_tokens, a.n_tokens,
+                 a.status);
+    return;
+  }
   const int64_t i0 = static_cast<int64_t>(blockIdx.x) * kAppendTokens;
   if (threadIdx.x < kAppendTokens) {
     int row = 0;
@@ -507,7 +514,7 @@ cudaError_t launch_pages_copy(const PagePool& p, const int32_t* src, const int32
 }
 
 cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t s) {
-  const int64_t blocks = ceil_div(a.n_tokens, kAppendTokens);
+  const int64_t blocks = ceil_div(a.n_tokens, kAppendTokens) + 1;
   return launch_ex(paged_append_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, 0, a);
 }
 
