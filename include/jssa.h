@@ -350,7 +350,8 @@ JSSA_API jssa_status jssa_calibrate(const jssa_layout* L, const void* Qc, const 
  * Workspace: jssa_paged_workspace_size() bytes, zeroed once with jssa_workspace_init(); it holds
  * the status word and scratch, and every call leaves it ready for the next, of another layout
  * too: one of the largest size serves several layouts in turn.  Calls that may
- * overlap on the GPU (other streams) need a workspace each.
+ * overlap on the GPU (other streams) need a workspace each.  After a JSSA_DEV_TIMEOUT of attention (a
+ * bounded wait gave up) its O and lse are undefined and the workspace has to be initialised again.
  *
  * Checks on the device: a sequence whose length is outside [0, max_pages * page_size], or whose
  * rows in q_begin are out of order, past n_tokens or more than its length, raises
@@ -480,7 +481,10 @@ JSSA_API jssa_status jssa_workspace_init(void* workspace, size_t ws_bytes, void*
  * normally: its device status has JSSA_DEV_TIMEOUT (jssa_read_device_status returns
  * JSSA_ERR_TIMEOUT), row (0, 0) has an empty selection (n_sel = 0, idx all -1; with the
  * attention inside the step, its output is the attention over the window alone, zero
- * without one) and the other rows are unaffected.  The launch disarms the request.
+ * without one) and the other rows are unaffected.  The launch disarms the request.  If the next
+ * launch is a jssa_paged_attn, its first CTA withholds one copy, or one warp's arrival where rows are
+ * few, if it has work; its waits give up after their own limit of a second, and the outputs are
+ * undefined, as after any timeout of that call.
  */
 JSSA_API jssa_status jssa_test_withhold_copy(void* workspace, size_t ws_bytes, int32_t wait_limit_us, void* stream);
 

@@ -291,7 +291,8 @@ def workspace_init(ws, stream=None):
 
 def arm_withheld_copy(ws, wait_limit_us: int, stream=None):
     """Arm the one-shot test of the bounded waits in this workspace: the next selection
-    launch withholds one bulk copy in row (0, 0) and gives up waiting after wait_limit_us."""
+    launch withholds one bulk copy in row (0, 0) and gives up waiting after wait_limit_us (a paged
+    attention withholds one in its first CTA and gives up after a second)."""
     w, n = _ws(ws)
     _check("jssa_test_withhold_copy", load().jssa_test_withhold_copy(w, n, wait_limit_us, _stream(stream)))
 

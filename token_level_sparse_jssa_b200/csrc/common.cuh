@@ -31,7 +31,7 @@ __device__ __forceinline__ void flag_error(int* status, int bit) {
 // Default limit of a bounded wait, and the one-shot test of the bounded waits that
 // jssa_test_withhold_copy() arms in the words after the status word: word 1 = 1 asks the
 // first CTA of row 0 of the next selection launch to withhold one bulk copy, word 2 is that
-// CTA's wait limit in microseconds.  The CTA disarms word 1 once it has read it.
+// CTA's wait limit in microseconds.  The CTA disarms word 1 once it has read it.  (Paged attention: paged_line.cuh.)
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
 struct WaitTest {
   bool withhold;

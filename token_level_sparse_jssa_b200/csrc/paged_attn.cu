@@ -198,12 +198,6 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
     return pieces[k % kPaPieces];
   };
   auto all_ok = [&](bool x) { return __all_sync(0xFFFFFFFFu, x) != 0; };
-  // after a timeout: each load under way arrives on one of its stage's phases
-  auto drain_loads = [&](uint32_t used) {
-    for (int i = 0; i < kNS; ++i)
-      if ((used >> i) & 1)
-        for (int t = 0; t < 2; ++t) mbar_wait_bounded(&kv_full[i], t, a.status, 1000000);
-  };
   auto release = [&](int k) {
     __syncwarp();
     if (lane == 0) mbar_arrive(&piece_empty[k % kPaPieces]);
@@ -530,13 +524,14 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
           ++tiles;
         }
       }
-      if (dead_s && lane == 0) drain_loads(used);
+      if (dead_s && lane == 0) drain_copies(kv_full, kNS, used, a.status);  // Q: the MMA thread
     } else if (warp == kValueWarp) {
       // ------------------------------------------------------------------ V
       const int box = lane;
       const bool on = box < p.nbox;
       uint32_t st = 1, st_par = 1, used = 0;
       bool ok = true;
+      const int armed = wait_test_armed(a);
       for (int piece = 0; ok; ++piece) {
         const Piece& s = take(piece, &ok);
         if (!ok) break;
@@ -553,7 +548,7 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
           uint64_t* bar = bad || edge_tile<C>(s.it, i) ? &edge_full[st] : &kv_full[st];
           if (lane == 0) mbar_arrive_expect_tx(bar, loads * p.box * (kDB * 128));
           __syncwarp();
-          if (pg >= 0)
+          if (pg >= 0 && !(armed == 1 && used == 0))
             tma_load_5d(kv_s + st * C::kStageBytes + box * p.box * (kDB * 128), &p.v, 0, row, 0, s.h, pg, bar);
           used |= 1u << st;
           st += 2;
@@ -561,7 +556,11 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
         }
         if (ok) release(piece);
       }
-      if (dead_s && lane == 0) drain_loads(used);
+      if (armed == 1) wait_test_disarm(a.status);
+      if (dead_s && lane == 0) {  // V comes on either barrier of its stage
+        drain_copies(kv_full, kNS, used, a.status);
+        drain_copies(edge_full, kNS, used, a.status);
+      }
     } else if (warp == kZeroWarp) {
       // ------------------------------------------------------------------ unseen V rows
       const bool on = lane < p.nbox;
@@ -740,6 +739,7 @@ __global__ void __launch_bounds__(Pa<D>::kThreads, 1) paged_attn_kernel(const __
         }
         umma_commit(&drain);  // every MMA and commit before it, in the error case too
         mbar_wait_bounded(&drain, 0, a.status);
+        if (dead_s) drain_copies(&q_full, 1, 1, a.status);
       }
       __syncwarp();
     }

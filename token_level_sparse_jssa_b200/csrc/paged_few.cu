@@ -147,16 +147,14 @@ __global__ void __launch_bounds__((Few<D, MT>::kThreads), 1) paged_few_kernel(co
         ++tiles;
       }
     }
-    if (dead_s && lane == 0)
-      for (int i = 0; i < kNS; ++i)
-        if ((used >> i) & 1)
-          for (int t = 0; t < 2; ++t) mbar_wait_bounded(&full[i], t, a.status, 1000000);
+    if (dead_s && lane == 0) drain_copies(full, kNS, used, a.status);
   } else {
     // ------------------------------------------------------------------ attention
     const int kw = warp % kKeyWarps, dw = warp / kKeyWarps;  // this warp's keys and columns
     const int r0 = lane >> 2, c2 = (lane & 3) * 2;           // its rows r0, r0 + 8, ..., its columns c2, c2 + 1 of 8
     uint32_t st = 0, st_par = 0, tiles = 0, all_par = 0;
     bool ok = true;
+    const int armed = warp == 7 ? wait_test_armed(a) : 0;
     auto meet = [&]() {
       __syncwarp();
       if (lane == 0) mbar_arrive(&all_bar);
@@ -318,7 +316,7 @@ __global__ void __launch_bounds__((Few<D, MT>::kThreads), 1) paged_few_kernel(co
         if (m[y] == -INFINITY) l[y] = 0.f;
         if ((lane & 3) == 0) m_s[warp][r0 + 8 * y] = m[y], l_s[warp][r0 + 8 * y] = l[y];
       }
-      ok = meet();
+      ok = all_ok(armed != 1) && meet();
       if (!ok) break;
       auto row_max = [&](int r) {
         float M = -INFINITY;
@@ -415,6 +413,7 @@ __global__ void __launch_bounds__((Few<D, MT>::kThreads), 1) paged_few_kernel(co
       __syncwarp();
       if (lane == 0) mbar_arrive(&piece_empty[piece % kPaPieces]);
     }
+    if (armed == 1) wait_test_disarm(a.status);
   }
   __syncthreads();
 }

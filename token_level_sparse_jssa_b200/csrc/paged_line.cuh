@@ -271,6 +271,7 @@ __device__ __forceinline__ Start line_start(const PaParams& p, const int64_t* se
   return {cuts, at, b0, h0, j0, idle};
 }
 
+// The bounded waits of a CTA.  After a timeout the outputs of the call are undefined.
 struct Waiter {
   volatile int* dead;
   int* status;
@@ -300,6 +301,25 @@ struct Waiter {
     }
   }
 };
+
+// The armed test of the waits (common.cuh): one warp of the first CTA reads the request while the line is worked out, and
+// withholds something that other warps wait for.  Their waits give up after their own limit (a shorter one for this
+// CTA would have to be read at every wait).
+__device__ __forceinline__ int wait_test_armed(const PagedAttnArgs& a) {
+  int armed = 0;
+  if (blockIdx.x == 0 && (threadIdx.x & 31) == 0)  // volatile: the load is not to be moved to where it is looked at
+    asm volatile("ld.global.cg.b32 %0, [%1];" : "=r"(armed) : "l"(a.status + 1));
+  return armed;
+}
+
+// In a CTA that has given up: the copies into the stages in `used`, which end a phase of their barriers, land.  One of
+// a barrier's two phases has always ended, and the wait for the other is short where no copy will end it (a
+// copy lands within microseconds).
+__device__ __forceinline__ void drain_copies(uint64_t* bars, int n, uint32_t used, int* status) {
+  for (int i = 0; i < n; ++i)
+    if ((used >> i) & 1)
+      for (int t = 0; t < 2; ++t) mbar_wait_bounded(&bars[i], t, status, 1000000);
+}
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
