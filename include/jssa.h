@@ -335,7 +335,7 @@ JSSA_API jssa_status jssa_calibrate(const jssa_layout* L, const void* Qc, const 
  *               the pages up first, or release ends the sequence
  * Q heads as elsewhere: query head hq belongs to KV head hq / G, G = Hq / Hkv.
  * Supported: d in {64, 128, 256}, 1 <= G <= 128, page_size a multiple of 16, B <= 1024,
- * max_pages * page_size <= 2^30, a page of a pool below 2^33 elements.  Pool pointers 16-byte
+ * max_pages * page_size <= 2^30, a page of a pool below 2^34 elements.  Pool pointers 16-byte
  * aligned, strides multiples of 8 elements; pages, heads and rows of a pool must not overlap.
  * A contiguous cache [B, Hkv, T_cap, d] (T_cap a multiple of 16) is a pool of B pages of T_cap
  * rows with the table page_table[b, 0] = b: the calls below then fill and read the caches of

@@ -1,0 +1,36 @@
+"""Limits of the paged layouts and what the binding refuses of a workspace, on the CPU."""
+import ctypes as C
+
+import pytest
+import torch
+
+FAKE = 0x10000
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from token_level_sparse_jssa_b200 import build
+    build.build()
+    from token_level_sparse_jssa_b200 import _binding
+    return _binding.load()
+
+
+def _layout(Hkv, page, d, max_pages=1):
+    from token_level_sparse_jssa_b200 import PagedLayout
+    L = PagedLayout()
+    L.B, L.Hq, L.Hkv, L.d, L.page_size, L.n_pages, L.max_pages = 1, Hkv, Hkv, d, page, 1, max_pages
+    for st in (L.k_stride, L.v_stride):
+        st[0], st[1], st[2] = Hkv * page * d, page * d, d
+    return L
+
+
+@pytest.mark.parametrize("Hkv,page,d,code", [
+    (8, (1 << 24) - 16, 128, 0), (8, 1 << 24, 128, 2),            # 2^34 elements a page and just below
+    (64, (1 << 21) - 16, 128, 0), (64, 1 << 21, 128, 2), (65, 1 << 21, 128, 2),
+    (128, (1 << 21) - 16, 64, 0), (128, 1 << 21, 64, 2), (127, 1 << 21, 64, 0), (1, 1 << 26, 256, 2),
+])
+def test_a_page_has_less_than_two_to_the_34_elements(lib, Hkv, page, d, code):
+    L = _layout(Hkv, page, d)
+    # calls that return before any CUDA call, once the layout is found good
+    assert lib.jssa_pages_copy(C.byref(L), None, None, None, None, 0, None, None, 0, None) == code
+    assert lib.jssa_pages_fork(C.byref(L), None, None, 0, None, None, None, None, 0, None) == code

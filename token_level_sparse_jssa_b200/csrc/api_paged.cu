@@ -29,7 +29,7 @@ jssa_status check_paged(const jssa_paged_layout* L) {
   if (L->page_size % 16) return JSSA_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(L->max_pages) * L->page_size > (int64_t(1) << 30) ||
       static_cast<int64_t>(L->B) * L->max_pages > kInt31 ||
-      static_cast<int64_t>(L->Hkv) * L->page_size * (L->d / 8) > kInt31 - 4096)
+      static_cast<int64_t>(L->Hkv) * L->page_size * L->d >= (int64_t(1) << 34))
     return JSSA_ERR_UNSUPPORTED;
   return JSSA_OK;
 }

@@ -250,7 +250,7 @@ cudaError_t launch_pages_fork(const PageBook& k, const int32_t* src, const int32
 cudaError_t launch_pages_reserve(const PageBook& k, const int32_t* n_new, int32_t* copy_src, int32_t* copy_dst,
                                  int32_t* growers, int32_t* free_list, cudaStream_t s);
 cudaError_t launch_pages_release(const PageBook& k, const int32_t* ended, int window, int n_sinks, cudaStream_t s);
-// map: [n_pages]
+// map: [n_pages + 1]; the last one takes the number of pages in use
 cudaError_t launch_pages_compact(const PageBook& k, int32_t* src, int32_t* dst, int max_moves, int32_t* n_moves,
                                  int32_t* map, cudaStream_t s);
 cudaError_t launch_pages_copy(const PagePool& p, const int32_t* src, const int32_t* dst, int n, const int32_t* count,

@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(256) pages_copy_kernel(PagePool p, const int32
   if (count) n = max(0, min(n, count[0]));
   const int cpr = p.d / 8;
   const int vecs = p.Hkv * p.page_size * cpr;  // per page and pool (< 2^31, checked by the host)
-  const int chunks = (vecs + 256 * kCopyPer - 1) / (256 * kCopyPer);
+  const int chunks = (vecs - 1) / (256 * kCopyPer) + 1;  // every vector's number stays below 2^31
   const int64_t items = static_cast<int64_t>(n) * 2 * chunks;
   for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
     const int64_t pair = it / (2 * chunks);
