@@ -34,3 +34,19 @@ def test_a_page_has_less_than_two_to_the_34_elements(lib, Hkv, page, d, code):
     # calls that return before any CUDA call, once the layout is found good
     assert lib.jssa_pages_copy(C.byref(L), None, None, None, None, 0, None, None, 0, None) == code
     assert lib.jssa_pages_fork(C.byref(L), None, None, 0, None, None, None, None, 0, None) == code
+
+
+def test_a_workspace_of_repeated_or_spread_bytes_is_refused(monkeypatch):
+    # its size would count bytes that are not its own
+    import token_level_sparse_jssa_b200 as jssa
+    from token_level_sparse_jssa_b200 import _paged
+    monkeypatch.setattr(_paged, "_device", lambda: -1)      # where host tensors say they are
+    monkeypatch.setattr(_paged, "_stream", lambda stream, dev: None)
+    K = torch.zeros(2, 1, 16, 64, dtype=torch.bfloat16)
+    table = torch.zeros(1, 1, dtype=torch.int32)
+    L = jssa.make_paged_layout(K, K, table, 1)
+    none = torch.zeros(0, dtype=torch.int32)
+    jssa.pages_copy(L, K, K, none, none, None, torch.zeros(4096, dtype=torch.uint8))    # nothing to copy: no CUDA call
+    for ws in (torch.zeros(1, dtype=torch.uint8).expand(1 << 30), torch.zeros(4096, 2, dtype=torch.uint8)[:, 0]):
+        with pytest.raises(ValueError):
+            jssa.pages_copy(L, K, K, none, none, None, ws)

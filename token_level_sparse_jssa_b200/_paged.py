@@ -125,8 +125,8 @@ def _book(f, page_table, ref_count, seq_lens, dev):
 def _ws(ws, dev):
     if ws is None:
         return None, 0
-    if not isinstance(ws, Tensor) or ws.get_device() != dev:
-        _refuse(ws, "ws", dev, "workspace")
+    if not isinstance(ws, Tensor) or ws.get_device() != dev or not ws.is_contiguous():
+        _refuse(ws, "ws", dev, "contiguous workspace")
     return ws.data_ptr(), ws.nbytes
 
 
