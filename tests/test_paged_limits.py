@@ -50,3 +50,25 @@ def test_a_workspace_of_repeated_or_spread_bytes_is_refused(monkeypatch):
     for ws in (torch.zeros(1, dtype=torch.uint8).expand(1 << 30), torch.zeros(4096, 2, dtype=torch.uint8)[:, 0]):
         with pytest.raises(ValueError):
             jssa.pages_copy(L, K, K, none, none, None, ws)
+
+
+@pytest.mark.parametrize("value", [1 << 31, (1 << 32) + 5, 1 << 40])
+def test_bounds_and_windows_past_31_bits_are_refused(value, monkeypatch):
+    # an int32 argument would be cut to its low bits: a window of 2^32 + 5 tokens to one of 5
+    import token_level_sparse_jssa_b200 as jssa
+    from token_level_sparse_jssa_b200 import _paged
+    monkeypatch.setattr(_paged, "_device", lambda: -1)
+    monkeypatch.setattr(_paged, "_stream", lambda stream, dev: None)
+    K = torch.zeros(2, 1, 16, 64, dtype=torch.bfloat16)
+    table, ref, lens, begin = (torch.zeros(n, dtype=torch.int32) for n in ((1, 1), 2, 1, 2))
+    L = jssa.make_paged_layout(K, K, table, 1)
+    Q, O, ws = torch.zeros(0, 1, 64, dtype=torch.bfloat16), torch.zeros(0, 1, 64), torch.zeros(256, dtype=torch.uint8)
+    for max_q, window, sinks in ((value, 0, 0), (1, value, 0), (1, 8, value)):
+        with pytest.raises(ValueError):
+            jssa.paged_attn(L, Q, K, K, table, begin, max_q, lens, window, sinks, 0.1, O, None, ws)
+    jssa.paged_attn(L, Q, K, K, table, begin, 1, lens, (1 << 31) - 1, 0, 0.1, O, None, ws)   # no rows: no CUDA call
+    for window, sinks in ((value, 0), (8, value)):
+        with pytest.raises(ValueError):
+            jssa.pages_release(L, None, window, sinks, table, ref, lens, ws)
+    with pytest.raises(ValueError):
+        jssa.paged_workspace_size(L, value)

@@ -130,6 +130,12 @@ def _ws(ws, dev):
     return ws.data_ptr(), ws.nbytes
 
 
+def _fits(*ints):
+    """Refuses what the C ABI's int32 would silently cut (negative values are its own to refuse)."""
+    if max(ints) >= 1 << 31:
+        raise ValueError(f"{ints}: values below 2**31 expected")
+
+
 def make_paged_layout(K: torch.Tensor, V: torch.Tensor, page_table: torch.Tensor, Hq: int,
                       out_dtype: int = OUT_F32) -> PagedLayout:
     """Layout from pools K and V [n_pages, Hkv, page_size, d] (any strides with a contiguous last
@@ -148,6 +154,7 @@ def make_paged_layout(K: torch.Tensor, V: torch.Tensor, page_table: torch.Tensor
 
 
 def paged_workspace_size(L: PagedLayout, max_q_len: int = 0) -> int:
+    _fits(max_q_len)
     n = C.c_size_t(0)
     _check("jssa_paged_workspace_size", load().jssa_paged_workspace_size(C.byref(L), max_q_len, C.byref(n)))
     return n.value
@@ -184,6 +191,7 @@ def paged_attn(L, Q, K, V, page_table, q_begin, max_q_len: int, seq_lens, window
     an optional sliding window (window > 0) and n_sinks first tokens that stay visible."""
     dev, f = _device(), _facts(L)
     Hq, _, d = f.heads
+    _fits(max_q_len, window, n_sinks)
     q, n, qs = _rows(Q, Hq, d, "Q", dev)
     w, nw = _ws(ws, dev)
     code = load().jssa_paged_attn(
@@ -223,6 +231,7 @@ def pages_release(L, ended, window: int, n_sinks: int, page_table, ref_count, se
     """Give up all pages of the sequences with ended[b] != 0 and, with window > 0, the others' pages
     behind their last `window` tokens that hold none of the first n_sinks."""
     dev, f = _device(), _facts(L)
+    _fits(window, n_sinks)
     code = load().jssa_pages_release(
         C.byref(L), None if ended is None else _packed(ended, _I32, f.seq, "ended", dev), window, n_sinks,
         *_book(f, page_table, ref_count, seq_lens, dev), *_ws(ws, dev), _stream(stream, dev))
