@@ -21,7 +21,6 @@ enum : int {
   DEVFLAG_BAD_INDEX = 2,     // an index outside the candidate range (skipped)
   DEVFLAG_BAD_NSEL = 4,      // n_sel outside [0, k] (clamped)
   DEVFLAG_TIMEOUT = 8,       // a bounded wait gave up
-  DEVFLAG_NO_PAGES = 16,     // too few free pages or table entries (nothing changed)
 };
 
 __device__ __forceinline__ void flag_error(int* status, int bit) {
@@ -31,7 +30,7 @@ __device__ __forceinline__ void flag_error(int* status, int bit) {
 // Default limit of a bounded wait, and the one-shot test of the bounded waits that
 // jssa_test_withhold_copy() arms in the words after the status word: word 1 = 1 asks the
 // first CTA of row 0 of the next selection launch to withhold one bulk copy, word 2 is that
-// CTA's wait limit in microseconds.  The CTA disarms word 1 once it has read it.  (Paged attention: paged_line.cuh.)
+// CTA's wait limit in microseconds.  The CTA disarms word 1 once it has read it.
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
 struct WaitTest {
   bool withhold;
@@ -148,19 +147,6 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], const void* 
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(smem_u32(p)));
-}
-// The same from an address in the shared window.
-__device__ __forceinline__ void ldmatrix_x4_at(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void ldmatrix_x4_trans_at(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
 }
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
   uint32_t y;

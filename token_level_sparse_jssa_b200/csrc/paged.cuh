@@ -5,6 +5,9 @@
 
 namespace jssa {
 
+// A bit of the device status word beside those of common.cuh.
+constexpr int DEVFLAG_NO_PAGES = 16;  // too few free pages or table entries (nothing changed)
+
 // The packed rows of one sequence's newest tokens: rows [q0, q0 + nq) at positions
 // [len - nq, len).
 struct NewTokens {
