@@ -6,8 +6,8 @@
 // arguments alone (the lowest free pages are taken, in sequence order), so the kernels use
 // scans where order matters and atomics only for counts, whose sums do not depend on it.
 //
-// Measured on a B200 (device time of a launch on its own; an empty one takes 4 us).  Serving-size book, 256
-// or 128 sequences, 8,192 pages: fork 5.4 us, reserve 12.3, release 6.1, compact 12.3: chains of a few
+// Measured on a B200 (a graph of one launch between two events).  Serving-size book, 256
+// or 128 sequences, 8,192 pages: fork 6.3 us, reserve 14.0, release 5.9, compact 13.9: chains of a few
 // dependent reads each, so each is one launch of one block (reserve), a block per row, or one cluster
 // (compact).  Page copies: 2,000 pages of 256 KB in 169 us, 0.97 of the measured copy rate; 180 in 18
 // us.  Append of 25,000 rows of 8 heads 39-41 us (5.2 TB/s), of 64 rows 7.4.
@@ -61,8 +61,7 @@ __device__ __forceinline__ int clamp_len(int len, const PageBook& k, bool* bad) 
 // A table entry past its sequence's length (a sequence that gave tokens back) still counts as a holder of its page;
 // before fork or reserve writes over it, the page is given up.  A page that is counted free already keeps its count, and
 // the entry, which cannot be right, is cleared.
-__device__ __forceinline__ void give_up(const PageBook& k, int32_t* entry) {
-  const int p = *entry;
+__device__ __forceinline__ void give_up(const PageBook& k, int32_t* entry, int p) {  // p: the entry's page
   if (p < 0 || p >= k.n_pages) return;
   if (atomicSub(k.ref + p, 1) <= 0) {
     atomicAdd(k.ref + p, 1);
@@ -97,13 +96,14 @@ __global__ void __launch_bounds__(256) pages_fork_kernel(PageBook k, const int32
   int32_t* to = k.table + static_cast<int64_t>(t) * k.max_pages;
   bool bad_page = false;
   for (int j = threadIdx.x; j < k.max_pages; j += blockDim.x) {
+    const int held = to[j];
     int p = j < used ? from[j] : -1;
     if (p >= k.n_pages) {
       bad_page = true;
       p = -1;
     }
     if (p >= 0) atomicAdd(k.ref + p, 1);
-    give_up(k, to + j);
+    give_up(k, to + j, held);
     to[j] = p < 0 ? -1 : p;
   }
   if (bad_page) flag_error(k.status, DEVFLAG_BAD_INDEX);
@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(1024) pages_reserve_kernel(PageBook k, const i
   };
   __threadfence_block();
   fail = __syncthreads_or(fail) != 0;
-  if (!fail) past_entries([&](int32_t* e) { give_up(k, e); });
+  if (!fail) past_entries([&](int32_t* e) { give_up(k, e, *e); });
   if (!fail && part_page) {
     atomicAdd(growers + 2 * static_cast<int64_t>(last), 1);
     atomicMax(growers + 2 * static_cast<int64_t>(last) + 1, b + 1);
