@@ -395,7 +395,8 @@ JSSA_API jssa_status jssa_paged_append_kv(const jssa_paged_layout* L, const void
  *   t <= p  and  (t > p - window or t < n_sinks)   (window > 0: the sliding window and the sinks)
  * logits = sm_scale * q . k_t, softmax and sums in fp32; O = sum_t p_t v_t / sum_t p_t.  In the product
  * with v_t a weight p_t keeps 16 bits (2^-16 of itself) if O is fp32 or the sequence has at most 128 / G (rounded
- * down) new tokens, and is rounded to bf16 otherwise: for each sequence by its own tokens, whatever max_q_len says.
+ * down) new tokens, and is rounded to bf16 otherwise (d = 64 and 128: with one exponential in 16 good to 7.5e-5
+ * only, in the sums and lse too): for each sequence by its own tokens, whatever max_q_len says.
  *   Q    device bf16, element (row i, head hq, e) at Q[i*q_stride + hq*d + e], q_stride >= Hq*d, a
  *        multiple of 8; 16-byte aligned
  *   O    [n_tokens, Hq, d] fp32 or bf16 (out_dtype), contiguous, 16-byte aligned

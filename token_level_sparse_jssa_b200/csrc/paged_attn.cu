@@ -16,7 +16,7 @@
 // balanced, and the host needs no lengths.  An item that is cut leaves unnormalised partial
 // outputs with their maxima and sums in the workspace.  They are merged in the order of the cuts, so
 // results do not depend on timing: items of many rows by a second launch, whose blocks come as CTAs
-// leave (the last CTA alone took 2 us per piece: 500 tokens of one head over 40K keys 79 us, now 42),
+// leave (the last CTA alone took 2 us per piece: 500 tokens of one head over 40K keys 79 us, so 42),
 // the others by the CTA that finishes them last.
 //
 // Per tile:  S = Q K^T (M = 128 rows, N = keys), P = exp2(S - m) by one thread per row, written
@@ -38,15 +38,18 @@
 // the V rows of a loaded tile that no query of the item sees: P is 0 there, but such rows may
 // hold infinities or NaN.
 //
-// What bounds it, measured on a B200 (d = 128, 4 query heads per KV head): 1.1 to 1.2 PFLOP/s of
-// bf16 on prompt chunks (4 x 512 tokens at 32K: 920-940 us, 0.71 of the measured burst matrix
-// rate; an 8K prompt from nothing: 540-570 us).  A tile of two query tiles takes about 3,600 cycles for
-// 2,048 of matrix work: a row's softmax (load of S, maximum, 128 exponentials, store of P: 2,300
-// cycles while the other warpgroup shares the pipes) and its products follow one another.  Tried
-// and slower: tiles of 64 keys with two S slots per stream (the N = 64 score MMAs take as long
-// as N = 128 ones: 1,427 us against 950), four softmax warpgroups on half tiles (1,430), S read
-// twice in chunks (1,277).  The products begin with the first half of P (about 1 %); a few of the
-// exponentials go to the FMA pipe (none 983, an eighth or a sixteenth 950, a quarter 1,012 us).
+// What bounds it, measured on a B200 (d = 128, 4 query heads per KV head, bf16 output): 4 x 512 tokens at 32K 1,079 us
+// and an 8K prompt from nothing 585 us, call after call at the power-capped clock: 1.01 and 0.94 PFLOP/s of bf16, 0.72
+// and 0.67 of the matrix rate measured under that cap.  The 8K prompt with d = 64 takes 480 us (0.57 PFLOP/s:
+// the same softmax for half the matrix work), with d = 256 and 16 heads 628 (0.88), with an fp32 output 872 (its second
+// part of P is half as much matrix work again).
+// A tile of two query tiles takes about 3,600 cycles for 2,048 of matrix work: a row's softmax (load of S, maximum, 128
+// exponentials, store of P: 2,300 cycles while the other warpgroup shares the pipes) and its products follow one
+// another; neither the tensor pipe (43 %) nor the issue slots (31 %) are full.  Tried and slower (short runs,
+// before the power cap): tiles of 64 keys with two S slots per stream (the N = 64 score MMAs take as long as N = 128
+// ones: 1,427 us against 950), four softmax warpgroups on half tiles (1,430), S read twice in chunks (1,277).
+// The products begin with the first half of P (about 1 %); a few of the exponentials go to the FMA pipe (none 983,
+// an eighth or a sixteenth 950, a quarter 1,012 us).
 //
 // Every wait is bounded; on a timeout the kernel raises DEVFLAG_TIMEOUT, all roles leave their
 // loops, copies and MMAs in flight are drained, and tensor memory is freed.

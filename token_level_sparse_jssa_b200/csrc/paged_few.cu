@@ -8,8 +8,8 @@
 // it scores them with 16 x 8 x 16 MMAs, keeps its own maximum, sum and output rows in registers, and
 // waits for nobody until the piece ends.  Then the warps' rows are added up in shared memory.
 //
-// Measured on a B200: one token over 4 x 100K-131K rows of 8 heads, d = 128, 295 us, the rate of a plain
-// copy; with the 128-row tiles 303, and 333 under sustained load.  One token of a 2K sequence 14.5 us
+// Measured on a B200: one token over 4 x 100K-131K rows of 8 heads, d = 128, 299 us, the rate of a plain
+// copy; with the 128-row tiles 303, and 333 under sustained load.  One token of a 2K sequence 15 us
 // (16.7), of 64 sequences of 700-3,000 tokens 93 us (105), of 16 with d = 64 49 us (62).  Two query rows
 // over 8 windows of 1,024 keys, d = 256: 28 us, of which 5 until the first keys arrive, 11 for 67 MB of
 // keys and values, and 10 to add up the warps and merge the pieces.
@@ -451,8 +451,10 @@ cudaError_t launch(const PagedAttnArgs& a, int num_sms, cudaStream_t s) {
 
 }  // namespace
 
-// Two row tiles pay for d = 64 only: 8 tokens of 4-head groups over 16 caches of 8K-16K rows took 59 us here and
-// 62 in the large kernel; for d = 128, where a tile must shrink to 64 keys, over 8 caches of 5K 69 and 49.
+// Up to 16 rows, both sides measured: 16 rows over 8 caches of 5K, d = 128, 41.3 us here and 52.7 in the large kernel;
+// d = 256 76.6 and 75.2, but 4 rows 68.3 and 71.9.  Two row tiles pay for d = 64 only: 8 tokens of 4-head groups over 16
+// caches of 12K and 8 KV heads 105 us here and 120 in the large kernel; for d = 128, where a tile must shrink to 64
+// keys, over 8 caches of 5K 69 and 49 (short runs).
 bool paged_few_rows(int d, int64_t rows) { return rows <= (d == 64 ? 32 : 16); }
 
 cudaError_t launch_paged_few(const PagedAttnArgs& a, int num_sms, cudaStream_t s) {

@@ -182,6 +182,11 @@ __device__ __forceinline__ void line_lengths(const PaParams& p, int64_t* seq_uni
       const Item it = item_at<C>(p, t.nq, t.len, j);
       const int64_t u = item_units<C>(it);
       n += u;
+      // What one more piece of an item adds to its merge, in units (a tile of one query tile is one: about 1 us).  Rows
+      // merged by a CTA: a unit for 8,192 values.  A quarter and four times that: one token of 16-head groups over 40K
+      // 28.0 us -> 29.9 and 33.4; 100 tokens of one head over 40K 70.3 -> 74.4 and 91.1.  Rows merged by the second launch:
+      // 0.15.  None and four times that: 500 tokens of one head over 40K 41.7 -> 44.5 and 43.4; 64 with
+      // d = 256 over 20K 28.4 -> 38.1 and 32.9.
       const float cost = tall_item<C>(it, p.G) ? 0.15f : it.ntok * p.G * (C::kD / 8192.f);
       merge = fmaxf(merge, u * cost);
     }
