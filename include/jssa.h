@@ -345,7 +345,8 @@ JSSA_API jssa_status jssa_calibrate(const jssa_layout* L, const void* Qc, const 
  * sequence: token row i of sequence b is row q_begin[b] + i for i < q_begin[b+1] - q_begin[b]
  * (q_begin: device int32 [B+1], ascending, q_begin[B] <= n_tokens) and stands at position
  * seq_lens[b] - (q_begin[b+1] - q_begin[b]) + i: seq_lens counts the new tokens.  A sequence
- * may have none.  Rows at and past q_begin[B] are neither read nor written.
+ * may have none.  Rows at and past q_begin[B] (and before q_begin[0]) take no part: whatever stands
+ * there changes nothing, and no output row there is written.
  *
  * Workspace: jssa_paged_workspace_size() bytes, zeroed once with jssa_workspace_init(); it holds
  * the status word and scratch, and every call leaves it ready for the next, of another layout
